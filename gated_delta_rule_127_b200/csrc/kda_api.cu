@@ -30,6 +30,8 @@ constexpr int kMaxDevices = 64;
 std::mutex g_flag_mutex;
 unsigned int* g_flag_addr[kMaxDevices] = {};
 
+}  // namespace
+
 // Device address of g_device_flags for the current device (looked up once per device).
 cudaError_t device_flags_ptr(unsigned int** out) {
     int dev = 0;
@@ -46,6 +48,8 @@ cudaError_t device_flags_ptr(unsigned int** out) {
     *out = g_flag_addr[dev];
     return cudaSuccess;
 }
+
+namespace {
 
 std::atomic<uint32_t> g_wait_polls{kDefaultWaitPolls};
 

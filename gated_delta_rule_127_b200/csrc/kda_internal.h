@@ -83,4 +83,77 @@ cudaError_t launch_chunk_scan(const ChunkArgs& a);
 // does): o <- o / rms(o) * norm_weight * sigmoid(out_gate), one warp per (token, head).
 cudaError_t launch_output_epilogue(const ChunkArgs& a);
 
+// ---- latent attention (kda_mla_api.cu checks the arguments, kda_mla_*.cu hold the kernels)
+
+// Device address of the current device's sticky flag word (looked up once per device).
+cudaError_t device_flags_ptr(unsigned int** out);
+
+constexpr int kMlaLatent = 512, kMlaPe = 64;             // cached channels per token
+constexpr int kMlaNope = 128, kMlaV = 128;               // per-head channels of the expanded form
+constexpr int kMlaQk = kMlaNope + kMlaPe, kMlaKv = kMlaNope + kMlaV;
+
+// The paged latent cache and the sequences' places in it.
+struct MlaCache {
+    void* latent;       // [num_pages, page_size, 512] bf16 or e4m3
+    void* pe;           // [num_pages, page_size, 64] bf16
+    float* scale;       // [num_pages, page_size], e4m3 only
+    const int32_t* page_table;  // [B, max_pages]
+    int64_t num_pages;
+    int page_size, page_shift, max_pages;
+    bool e4m3;
+};
+
+struct MlaCacheCopyArgs {  // kda_mla_cache_write and kda_mla_cache_read
+    MlaCache cache;
+    void* latent;  // [T, 512] of the packed side, fp32 or bf16
+    void* pe;      // [T, 64]
+    const int32_t* cu_seqlens;  // may be NULL: equal lengths T / B
+    const int32_t* lens;        // write: seq_lens; read: starts (may be NULL)
+    int64_t T;
+    int B;
+    bool fp32;  // the packed side's type
+    unsigned int* flags;
+    cudaStream_t stream;
+};
+
+struct MlaDecodeArgs {
+    const void* q_latent;
+    const void* q_pe;
+    MlaCache cache;
+    const int32_t* seq_lens;
+    int B, S, H;
+    float scale;
+    bool o_fp32;
+    void* o;
+    float* lse;  // may be NULL
+    void* workspace;  // NULL: no sequence is split
+    unsigned int* flags;
+    uint32_t wait_polls;
+    cudaStream_t stream;
+};
+
+struct MlaPrefillArgs {
+    const void* q;
+    const void* kv;
+    const void* k_pe;
+    const int32_t* cu_q;  // may be NULL: equal lengths
+    const int32_t* cu_k;
+    int64_t Tq, Tk;
+    int B, H;
+    bool causal;
+    float scale;
+    bool o_fp32;
+    void* o;
+    float* lse;  // may be NULL
+    unsigned int* flags;
+    uint32_t wait_polls;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_mla_cache_write(const MlaCacheCopyArgs& a);
+cudaError_t launch_mla_cache_read(const MlaCacheCopyArgs& a);
+size_t mla_decode_workspace_size(int B, int S, int H);
+cudaError_t launch_mla_decode(const MlaDecodeArgs& a);
+cudaError_t launch_mla_prefill(const MlaPrefillArgs& a);
+
 }  // namespace kda

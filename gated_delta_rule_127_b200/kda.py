@@ -19,8 +19,9 @@ INCLUDE_DIR = os.path.join(os.path.dirname(_HERE), "include")
 HEADER_PATH = os.path.join(INCLUDE_DIR, "kda.h")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT, KDA_ERR_DEVICE_CHECK = range(6)
-KDA_BF16, KDA_FP32 = 0, 1
+KDA_BF16, KDA_FP32, KDA_E4M3 = 0, 1, 2
 KDA_DEVFLAG_CU_SEQLENS, KDA_DEVFLAG_DECAY_RANGE, KDA_DEVFLAG_TIMEOUT = 0x1, 0x2, 0x4
+KDA_DEVFLAG_PAGE_TABLE, KDA_DEVFLAG_SEQ_LENS = 0x8, 0x10
 KDA_OPT_SCALAR_GATE, KDA_OPT_L2NORM_QK, KDA_OPT_BETA_LOGITS, KDA_OPT_OUTPUT_NORM_GATE = 0x1, 0x2, 0x4, 0x8
 
 _lib = None
@@ -59,6 +60,18 @@ def load_library() -> ctypes.CDLL:
     lib.kda_chunk_fwd_ex.restype = i32
     lib.kda_decode_step_ex.argtypes = lib.kda_decode_step.argtypes[:-1] + [ctypes.c_uint32, vp, vp, ctypes.c_float, vp]
     lib.kda_decode_step_ex.restype = i32
+    f32 = ctypes.c_float
+    lib.kda_mla_cache_write.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, vp, vp, vp, vp, i64, i32, i32, vp]
+    lib.kda_mla_cache_write.restype = i32
+    lib.kda_mla_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, i32, i32, i32, i32, vp, vp, vp]
+    lib.kda_mla_cache_read.restype = i32
+    lib.kda_mla_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.kda_mla_decode_workspace_size.restype = sz
+    lib.kda_mla_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i32, i32, f32, i32, i32, i32,
+                                   vp, vp, vp, sz, vp]
+    lib.kda_mla_decode.restype = i32
+    lib.kda_mla_prefill.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, vp, vp]
+    lib.kda_mla_prefill.restype = i32
     lib.kda_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.kda_get_device_status.restype = i32
     lib.kda_status_string.argtypes = [i32]
@@ -348,6 +361,239 @@ def _decode(entry, q, k, v, log_alpha, beta, state, o, dtype_o, stream, options=
     if st != KDA_OK:
         raise KdaError(st, entry)
     return o
+
+
+# ---- latent attention
+
+def _mla_cache_dtype(t: torch.Tensor) -> int:
+    if t.dtype == torch.float8_e4m3fn:
+        return KDA_E4M3
+    if t.dtype == torch.bfloat16:
+        return KDA_BF16
+    raise TypeError(f"cache_latent must be bfloat16 or float8_e4m3fn, got {t.dtype}")
+
+
+def _mla_index(t: torch.Tensor, what: str, shape) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table):
+    """Checks the paged cache's tensors; returns (dtype code, num_pages, page_size, B, max_pages)."""
+    code = _mla_cache_dtype(cache_latent)
+    if cache_latent.dim() != 3 or cache_pe.dim() != 3 or cache_latent.shape[:2] != cache_pe.shape[:2]:
+        raise ValueError("expected cache_latent [num_pages, page_size, d_latent], cache_pe [num_pages, page_size, d_pe]")
+    if cache_pe.dtype != torch.bfloat16:
+        raise TypeError(f"cache_pe must be bfloat16, got {cache_pe.dtype}")
+    if (cache_scale is None) == (code == KDA_E4M3):
+        raise ValueError("cache_scale goes with a float8_e4m3fn cache, and only with one")
+    if cache_scale is not None and (cache_scale.dtype != torch.float32 or cache_scale.shape != cache_latent.shape[:2]):
+        raise ValueError("cache_scale must be fp32 [num_pages, page_size]")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    return code, cache_latent.shape[0], cache_latent.shape[1], page_table.shape[0], page_table.shape[1]
+
+
+def _mla_call(device, stream, ts, new, call):
+    """Checks the tensors `ts`, allocates with new() on the stream of the call (so that a freed buffer is not
+    handed out again before the stream is past it) and launches with call(allocated, stream handle)."""
+    _check_cuda(ts, device)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _mla_call(device, stream, {}, new, call)
+    if stream is None:
+        got = new()
+        return got, call(got, torch.cuda.current_stream().cuda_stream)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream), device)
+    with torch.cuda.stream(s):
+        got = new()
+    return got, call(got, _stream_handle(stream))
+
+
+def kda_mla_cache_write(latent: torch.Tensor, pe: torch.Tensor, cache_latent: torch.Tensor, cache_pe: torch.Tensor,
+                        page_table: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *,
+                        cache_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes new tokens into the paged latent cache (kda_mla_cache_write in include/kda.h).
+
+    latent [T, 512], pe [T, 64] bf16 or fp32; cache_latent [num_pages, page_size, 512] bf16 or float8_e4m3fn (then
+    with cache_scale [num_pages, page_size] fp32), cache_pe [num_pages, page_size, 64] bf16; page_table
+    [B, max_pages] int32; seq_lens [B] int32, the new tokens included; cu_seqlens [B+1] int32 or None (the same
+    number of new tokens for each sequence).  The cache tensors are updated in place.
+    """
+    lib = load_library()
+    code, pages, page, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
+    if latent.dim() != 2 or pe.dim() != 2 or latent.shape[0] != pe.shape[0] or \
+            latent.shape[1] != cache_latent.shape[2] or pe.shape[1] != cache_pe.shape[2]:
+        raise ValueError("expected latent [T, d_latent] and pe [T, d_pe] with the cache's channels")
+    if latent.dtype != pe.dtype:
+        raise TypeError("latent and pe must share a dtype")
+    dt = _dtype_code(latent, "latent")
+    _mla_index(seq_lens, "seq_lens", (B,))
+    if cu_seqlens is not None:
+        _mla_index(cu_seqlens, "cu_seqlens", (B + 1,))
+    _, st = _mla_call(
+        latent.device, stream,
+        dict(latent=latent, pe=pe, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale,
+             page_table=page_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens), lambda: None,
+        lambda _, handle: lib.kda_mla_cache_write(
+            _ptr(latent), _ptr(pe), _ptr(cu_seqlens), _ptr(seq_lens), latent.shape[0], B, latent.shape[1], pe.shape[1],
+            dt, code, _ptr(cache_latent), _ptr(cache_pe), _ptr(cache_scale), _ptr(page_table), pages, page, width, handle))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_mla_cache_write")
+
+
+def kda_mla_cache_read(cache_latent: torch.Tensor, cache_pe: torch.Tensor, page_table: torch.Tensor,
+                       cu_seqlens: Optional[torch.Tensor], T: int, *, starts: Optional[torch.Tensor] = None,
+                       cache_scale: Optional[torch.Tensor] = None, latent: Optional[torch.Tensor] = None,
+                       pe: Optional[torch.Tensor] = None, dtype_o: Optional[torch.dtype] = None,
+                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Reads cached tokens back into packed arrays (kda_mla_cache_read in include/kda.h).
+
+    cu_seqlens [B+1] int32 (or None: T / B tokens each) says how many tokens of each sequence are read and where
+    they go; starts [B] int32 the first position of each (None: 0).  T: rows of the packed arrays.  Returns
+    (latent [T, 512], pe [T, 64]) in dtype_o (bf16 by default), the given tensors where there are any; rows
+    that nothing is read into are left as they were (undefined in arrays allocated here).
+    """
+    lib = load_library()
+    code, pages, page, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
+    if cu_seqlens is not None:
+        _mla_index(cu_seqlens, "cu_seqlens", (B + 1,))
+    if starts is not None:
+        _mla_index(starts, "starts", (B,))
+    T, dl, dp = int(T), cache_latent.shape[2], cache_pe.shape[2]
+    if T < 0:
+        raise ValueError("T must not be negative")
+    if dtype_o is None:
+        dtype_o = latent.dtype if latent is not None else pe.dtype if pe is not None else torch.bfloat16
+    for t, what, d in ((latent, "latent", dl), (pe, "pe", dp)):
+        if t is not None and (tuple(t.shape) != (T, d) or t.dtype != dtype_o):
+            raise ValueError(f"{what} must be {dtype_o} [{T}, {d}]")
+    device = cache_latent.device
+
+    def new():
+        return (torch.empty((T, dl), dtype=dtype_o, device=device) if latent is None else latent,
+                torch.empty((T, dp), dtype=dtype_o, device=device) if pe is None else pe)
+
+    got, st = _mla_call(
+        device, stream,
+        dict(cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale, page_table=page_table,
+             cu_seqlens=cu_seqlens, starts=starts, latent=latent, pe=pe), new,
+        lambda got, handle: lib.kda_mla_cache_read(
+            _ptr(cache_latent), _ptr(cache_pe), _ptr(cache_scale), _ptr(page_table), _ptr(cu_seqlens), _ptr(starts), T, B,
+            dl, dp, pages, page, width, code, _dtype_code(got[0], "dtype_o"), _ptr(got[0]), _ptr(got[1]), handle))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_mla_cache_read")
+    return got
+
+
+def kda_mla_decode_workspace_size(B: int, S: int, H: int, d_latent: int = 512, d_pe: int = 64) -> int:
+    return int(load_library().kda_mla_decode_workspace_size(B, S, H, d_latent, d_pe))
+
+
+def kda_mla_decode(q_latent: torch.Tensor, q_pe: torch.Tensor, cache_latent: torch.Tensor, cache_pe: torch.Tensor,
+                   page_table: torch.Tensor, seq_lens: torch.Tensor, *, softmax_scale: float,
+                   cache_scale: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                   dtype_o: Optional[torch.dtype] = None, lse: Optional[torch.Tensor] = None, output_lse: bool = False,
+                   workspace: Optional[torch.Tensor] = None, use_workspace: bool = True,
+                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Absorbed latent attention of S new tokens a sequence over the paged cache (kda_mla_decode in include/kda.h).
+
+    q_latent [B, S, H, 512], q_pe [B, S, H, 64] bf16; the cache as in kda_mla_cache_write; seq_lens [B] int32, the
+    new tokens included.  Returns (o [B, S, H, 512] in dtype_o, lse [B, S, H] fp32 or None).  A workspace of
+    kda_mla_decode_workspace_size bytes is allocated when none is given; with use_workspace=False none is
+    passed and no sequence is split over several SMs.
+    """
+    lib = load_library()
+    code, pages, page, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
+    if q_latent.dim() != 4 or q_pe.dim() != 4 or q_latent.shape[:3] != q_pe.shape[:3] or q_latent.shape[0] != B or \
+            q_latent.shape[3] != cache_latent.shape[2] or q_pe.shape[3] != cache_pe.shape[2]:
+        raise ValueError("expected q_latent [B, S, H, d_latent] and q_pe [B, S, H, d_pe] with the cache's channels")
+    _, S, H, dl = q_latent.shape
+    dp = q_pe.shape[3]
+    if q_latent.dtype != q_pe.dtype:
+        raise TypeError("q_latent and q_pe must share a dtype")
+    dq = _dtype_code(q_latent, "q_latent")
+    _mla_index(seq_lens, "seq_lens", (B,))
+    if dtype_o is None:
+        dtype_o = o.dtype if o is not None else q_latent.dtype
+    if o is not None and (tuple(o.shape) != (B, S, H, dl) or o.dtype != dtype_o):
+        raise ValueError(f"o must be {dtype_o} {[B, S, H, dl]}")
+    if lse is not None and (tuple(lse.shape) != (B, S, H) or lse.dtype != torch.float32):
+        raise ValueError(f"lse must be fp32 {[B, S, H]}")
+    device = q_latent.device
+    need = lib.kda_mla_decode_workspace_size(B, S, H, dl, dp) if use_workspace else 0
+
+    def new():
+        ws = None
+        if need > 0:
+            ws = workspace
+            if ws is None or ws.numel() * ws.element_size() < need:
+                ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return (torch.empty((B, S, H, dl), dtype=dtype_o, device=device) if o is None else o,
+                torch.empty((B, S, H), dtype=torch.float32, device=device) if lse is None and output_lse else lse, ws)
+
+    def call(got, handle):
+        ws = got[2]
+        return lib.kda_mla_decode(
+            _ptr(q_latent), _ptr(q_pe), _ptr(cache_latent), _ptr(cache_pe), _ptr(cache_scale), _ptr(page_table),
+            _ptr(seq_lens), B, S, H, dl, dp, pages, page, width, softmax_scale, dq, code, _dtype_code(got[0], "o"),
+            _ptr(got[0]), _ptr(got[1]), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), handle)
+
+    got, st = _mla_call(device, stream, dict(q_latent=q_latent, q_pe=q_pe, cache_latent=cache_latent, cache_pe=cache_pe,
+                                             cache_scale=cache_scale, page_table=page_table, seq_lens=seq_lens, o=o,
+                                             lse=lse, workspace=workspace), new, call)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_mla_decode")
+    return got[0], got[1]
+
+
+def kda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor] = None,
+                    cu_seqlens_k: Optional[torch.Tensor] = None, *, softmax_scale: float, num_seqs: Optional[int] = None,
+                    causal: bool = True, o: Optional[torch.Tensor] = None, dtype_o: Optional[torch.dtype] = None,
+                    lse: Optional[torch.Tensor] = None, output_lse: bool = False,
+                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Expanded latent attention over a packed batch (kda_mla_prefill in include/kda.h).
+
+    q [Tq, H, 192], kv [Tk, H, 256] (key part, value), k_pe [Tk, 64] bf16; cu_seqlens_q, cu_seqlens_k [B+1] int32 (both,
+    one or none; without them `num_seqs` sequences of equal lengths, default 1).  Returns
+    (o [Tq, H, 128] in dtype_o, lse [Tq, H] fp32 or None).  Rows behind the last sequence are not written.
+    """
+    lib = load_library()
+    if q.dim() != 3 or kv.dim() != 3 or k_pe.dim() != 2 or kv.shape[1] != q.shape[1] or k_pe.shape[0] != kv.shape[0]:
+        raise ValueError("expected q [Tq, H, d_nope + d_pe], kv [Tk, H, d_nope + dv], k_pe [Tk, d_pe]")
+    Tq, H, dqk = q.shape
+    Tk, dp = k_pe.shape
+    dn, dv = dqk - dp, kv.shape[2] - (dqk - dp)
+    if dn <= 0 or dv <= 0:
+        raise ValueError("the channels of q, kv and k_pe do not fit together")
+    if q.dtype != kv.dtype or q.dtype != k_pe.dtype:
+        raise TypeError("q, kv, k_pe must share a dtype")
+    dt = _dtype_code(q, "q")
+    given = [c for c in (cu_seqlens_q, cu_seqlens_k) if c is not None]
+    B = given[0].numel() - 1 if given else 1 if num_seqs is None else int(num_seqs)
+    for c, what in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k")):
+        if c is not None:
+            _mla_index(c, what, (B + 1,))
+    if dtype_o is None:
+        dtype_o = o.dtype if o is not None else q.dtype
+    if o is not None and (tuple(o.shape) != (Tq, H, dv) or o.dtype != dtype_o):
+        raise ValueError(f"o must be {dtype_o} {[Tq, H, dv]}")
+    if lse is not None and (tuple(lse.shape) != (Tq, H) or lse.dtype != torch.float32):
+        raise ValueError(f"lse must be fp32 {[Tq, H]}")
+    device = q.device
+
+    def new():
+        return (torch.empty((Tq, H, dv), dtype=dtype_o, device=device) if o is None else o,
+                torch.empty((Tq, H), dtype=torch.float32, device=device) if lse is None and output_lse else lse)
+
+    got, st = _mla_call(
+        device, stream, dict(q=q, kv=kv, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, o=o, lse=lse),
+        new, lambda got, handle: lib.kda_mla_prefill(
+            _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), Tq, Tk, B, H, dn, dp, dv,
+            1 if causal else 0, softmax_scale, dt, _dtype_code(got[0], "o"), _ptr(got[0]), _ptr(got[1]), handle))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_mla_prefill")
+    return got
 
 
 def kda_get_device_status(stream=None) -> Tuple[int, int]:

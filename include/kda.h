@@ -52,7 +52,11 @@ typedef enum {
     KDA_ERR_DEVICE_CHECK = 5   /* a device-side argument check failed (see kda_get_device_status) */
 } kda_status;
 
-typedef enum { KDA_BF16 = 0, KDA_FP32 = 1 } kda_dtype;
+typedef enum {
+    KDA_BF16 = 0,
+    KDA_FP32 = 1,
+    KDA_E4M3 = 2   /* 8-bit floating point, 4 exponent and 3 mantissa bits: the latent cache only */
+} kda_dtype;
 
 /* Sticky device flags returned by kda_get_device_status (bitwise OR). */
 #define KDA_DEVFLAG_CU_SEQLENS 0x1u   /* cu_seqlens[0] != 0, decreasing, or cu_seqlens[N] != T_total;
@@ -60,6 +64,10 @@ typedef enum { KDA_BF16 = 0, KDA_FP32 = 1 } kda_dtype;
 #define KDA_DEVFLAG_DECAY_RANGE 0x2u  /* reserved (bit kept for ABI stability): no path raises it, since
                                          every path is exact for every decay in (0, 1) */
 #define KDA_DEVFLAG_TIMEOUT 0x4u      /* a bounded inter-CTA wait gave up */
+#define KDA_DEVFLAG_PAGE_TABLE 0x8u   /* a page number that is used lies outside 0 .. num_pages - 1; its tokens
+                                         were taken as absent (kda_mla_*) */
+#define KDA_DEVFLAG_SEQ_LENS 0x10u    /* a length or start is negative, longer than the page table reaches, or
+                                         shorter than the new tokens; the sequence was skipped (kda_mla_*) */
 
 /*
  * Workspace bytes kda_chunk_fwd needs for these sizes (0 is a valid answer).
@@ -245,6 +253,113 @@ KDA_API kda_status kda_decode_step_ex(const void* q, const void* k, const void* 
                            kda_dtype dtype_qkv, kda_dtype dtype_gate, kda_dtype dtype_o,
                            void* o, uint32_t options, const void* out_gate, const float* norm_weight,
                            float norm_eps, void* stream);
+
+/*
+ * Latent attention, the other attention layer of the pages' stack.  Passage: "Kimi Linear: 표현력과
+ * 효율을 높인 어텐션 아키텍처(2025)", sections "KDA와 MLA의 3:1 하이브리드" and "NoPE 적용과 평가 결과":
+ * three KDA layers to one layer of multi-head latent attention (MLA), in which every token leaves one
+ * latent vector c_j (shared by the heads, from which keys and values are expanded) and one positional
+ * key p_j (shared by the heads; without positional encoding simply 64 further key channels).  For
+ * decoding, the expansion is absorbed into the query and the layer becomes attention over the latents
+ * themselves, with one key and value head (MQA).
+ *
+ *   expanded (kda_mla_prefill):  x_ij = scale (q_i^nope . k_j + q_i^pe . p_j),  o_i = sum_j softmax_j(x_ij) v_j
+ *   absorbed (kda_mla_decode):   x_ij = scale (q_i^latent . c_j + q_i^pe . p_j), o_i = sum_j softmax_j(x_ij) c_j
+ *
+ * The projections (down to c and p; k and v from c; q^latent = W_k^T q^nope; values from o) need weights
+ * and are the caller's.  Both forms can return lse_i = log sum_j e^{x_ij} (natural log).  A row that sees
+ * no key gives o = 0 and lse = -infinity.
+ *
+ * The paged latent cache, shared by the entry points below:
+ *   cache_latent [num_pages, page_size, d_latent]  dtype_cache (KDA_BF16 or KDA_E4M3)
+ *   cache_pe     [num_pages, page_size, d_pe]      bf16
+ *   cache_scale  [num_pages, page_size]            fp32, KDA_E4M3 only (NULL otherwise): a cached value is its
+ *                                                  code times its token's scale, a power of two in
+ *                                                  [2^-64, 2^120] (what kda_mla_cache_write stores)
+ *   page_table   [B, max_pages] int32 (device)     token j of sequence b lies in page page_table[b][j / page_size]
+ *                                                  at row j % page_size.  Entries past a sequence's length are
+ *                                                  not read.
+ *   page_size a power of two from 16 to 1024; num_pages * page_size < 2^31; d_latent = 512, d_pe = 64
+ *   (other sizes: KDA_ERR_UNSUPPORTED).
+ * cu_seqlens of these entry points: [B + 1] int32 (device) or NULL (equal lengths, T a multiple of B), as in
+ * kda_chunk_fwd, but cu_seqlens[B] may be less than T: the rows behind it are neither read nor written.
+ * What only the device can see (cu_seqlens, lengths, page numbers) raises KDA_DEVFLAG_CU_SEQLENS,
+ * KDA_DEVFLAG_SEQ_LENS or KDA_DEVFLAG_PAGE_TABLE; nothing outside the given arrays is touched.  The rows of
+ * a sequence skipped for its length (kda_mla_decode) or its cu_seqlens_k (kda_mla_prefill) get o = 0,
+ * lse = -infinity; those of a sequence with bad cu_seqlens_q are left as they were.
+ */
+
+/*
+ * Writes new tokens into the cache, quantising them on the way for KDA_E4M3.
+ *   latent     [T, d_latent], pe [T, d_pe]  dtype_in (KDA_BF16 or KDA_FP32; rounded to nearest)
+ *   cu_seqlens the new tokens of each sequence: n_b = cu_seqlens[b+1] - cu_seqlens[b]
+ *   seq_lens   [B] int32 (device): lengths that already count the new tokens; those of sequence b become its
+ *              positions seq_lens[b] - n_b .. seq_lens[b] - 1
+ * KDA_E4M3: a token's scale is the smallest power of two s in [2^-64, 2^120] with max |latent| <= 448 s (NaN
+ * ignored), its codes are latent / s rounded to nearest even (infinities become +-448, NaN stays NaN).
+ * Where two sequences' new tokens fall on the same pool row (a page given to both), its values are unspecified.
+ * T >= 0, B >= 1.
+ */
+KDA_API kda_status kda_mla_cache_write(const void* latent, const void* pe, const int32_t* cu_seqlens,
+                         const int32_t* seq_lens, int64_t T, int B, int d_latent, int d_pe,
+                         kda_dtype dtype_in, kda_dtype dtype_cache,
+                         void* cache_latent, void* cache_pe, float* cache_scale,
+                         const int32_t* page_table, int64_t num_pages, int page_size, int max_pages, void* stream);
+
+/*
+ * Reads cached tokens back into packed arrays (a chunked prefill expands its prefix from them).
+ *   cu_seqlens how many tokens of each sequence, n_b, and where they go in the packed arrays
+ *   starts     [B] int32 (device) or NULL (zeros): the positions read are starts[b] .. starts[b] + n_b - 1
+ *   latent     [T, d_latent], pe [T, d_pe]  dtype_o (KDA_BF16 or KDA_FP32)
+ * Rows of a skipped sequence and tokens of a bad page are left as they were.  T >= 0, B >= 1.
+ */
+KDA_API kda_status kda_mla_cache_read(const void* cache_latent, const void* cache_pe, const float* cache_scale,
+                         const int32_t* page_table, const int32_t* cu_seqlens, const int32_t* starts,
+                         int64_t T, int B, int d_latent, int d_pe, int64_t num_pages, int page_size, int max_pages,
+                         kda_dtype dtype_cache, kda_dtype dtype_o, void* latent, void* pe, void* stream);
+
+/* Workspace bytes kda_mla_decode wants for these sizes (0 is a valid answer).  Pure host function. */
+KDA_API size_t kda_mla_decode_workspace_size(int B, int S, int H, int d_latent, int d_pe);
+
+/*
+ * Absorbed latent attention of S new tokens per sequence over the paged cache (they have been written to it).
+ *   q_latent [B, S, H, d_latent], q_pe [B, S, H, d_pe]  dtype_q (KDA_BF16)
+ *   seq_lens [B] int32 (device): cached tokens, the new ones included.  New token s of sequence b is token
+ *            seq_lens[b] - S + s and sees itself and the tokens before it.  Length 0 is allowed.
+ *   o        [B, S, H, d_latent] dtype_o (KDA_BF16 or KDA_FP32);  lse [B, S, H] fp32 or NULL
+ *   workspace  device scratch, 16-byte aligned, of kda_mla_decode_workspace_size bytes, or NULL / 0 bytes: then
+ *              no sequence is split over several SMs (slow for few long sequences).  Its contents on entry do not
+ *              matter.  Calls that can run at the same time need a workspace each.
+ *   B >= 0 (0 launches nothing), S >= 1, H >= 1, S * H <= 65535
+ * Arithmetic: products of bf16 values with fp32 accumulation; softmax statistics and the output are held in
+ * fp32; the weights enter the second product in bf16.  With KDA_E4M3 the codes are multiplied as they are and
+ * queries and weights enter as two e4m3 parts each, which carry as many bits as bf16.
+ */
+KDA_API kda_status kda_mla_decode(const void* q_latent, const void* q_pe, const void* cache_latent,
+                         const void* cache_pe, const float* cache_scale, const int32_t* page_table,
+                         const int32_t* seq_lens, int B, int S, int H, int d_latent, int d_pe,
+                         int64_t num_pages, int page_size, int max_pages, float softmax_scale,
+                         kda_dtype dtype_q, kda_dtype dtype_cache, kda_dtype dtype_o, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Expanded latent attention over a packed batch.
+ *   q    [Tq, H, d_nope + d_pe]  dtype_qkv (KDA_BF16)    per head: the part without position, then the positional part
+ *   kv   [Tk, H, d_nope + dv]    dtype_qkv               per head: the key's expanded part, then the value
+ *   k_pe [Tk, d_pe]              dtype_qkv               the positional key, shared by the heads
+ *   cu_seqlens_q, cu_seqlens_k   the queries and the keys of each sequence.  cu_seqlens_k = NULL: equal key
+ *                                lengths, Tk a multiple of B.
+ *   causal   1: query i of a sequence with n_q queries and n_k keys sees keys j <= i + n_k - n_q (the last query
+ *            sees the last key); 0: every query sees all n_k keys
+ *   o    [Tq, H, dv] dtype_o (KDA_BF16 or KDA_FP32);  lse [Tq, H] fp32 or NULL
+ *   d_nope = 128, d_pe = 64, dv = 128;  Tq, Tk >= 0, B >= 1, 1 <= H <= 65535
+ * Arithmetic: products of bf16 values with fp32 accumulation; softmax statistics and the output are held in
+ * fp32; the weights enter the second product in bf16.  No workspace.
+ */
+KDA_API kda_status kda_mla_prefill(const void* q, const void* kv, const void* k_pe, const int32_t* cu_seqlens_q,
+                         const int32_t* cu_seqlens_k, int64_t Tq, int64_t Tk, int B, int H, int d_nope, int d_pe,
+                         int dv, int causal, float softmax_scale, kda_dtype dtype_qkv, kda_dtype dtype_o,
+                         void* o, float* lse, void* stream);
 
 /*
  * Waits for `stream`, then reads and clears the sticky device flags (KDA_DEVFLAG_*) of the current
