@@ -1,0 +1,91 @@
+// kda_mla_sm100.cuh -- what the latent-attention kernels add to kda_sm100.cuh: tensor-core products of bf16 and
+// e4m3 operands (kind::f16, kind::f8f6f4), untiled bulk copies, and bounded waits that end together.
+#pragma once
+
+#include "kda_common.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace sm100 {
+
+// Instruction descriptors with fp32 accumulation for bf16 and e4m3 operands.  a_mn / b_mn: the operand is stored
+// MN-major (M or N contiguous) instead of K-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// K = 16 bf16 values, both operands in shared memory
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A in tensor memory: lane = row, each 32-bit column two consecutive values along K
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// K = 32 e4m3 values
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Untiled copy into shared memory (16-byte aligned addresses and size), counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The waits of a block whose warps have different roles.  A wait that gives up (after `polls` polls or 2 s) raises
+// KDA_DEVFLAG_TIMEOUT and the block's abort word, at which every other wait of the block gives up too, so that
+// all roles leave their loops, drain what they have in flight (drain(), default bound) and meet at the end.
+struct RoleWait {
+    uint32_t polls;
+    volatile uint32_t* abort_word;  // shared memory
+    unsigned int* flags;
+
+    __device__ __forceinline__ bool aborted() const { return *abort_word != 0u; }
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        WaitBudget budget;
+        for (uint32_t i = 0; i < polls; ++i) {
+            if (mbar_poll(bar, parity)) return true;
+            if ((i & 7u) == 7u && aborted()) return false;
+            if (budget.expired()) break;
+        }
+        *abort_word = 1u;
+        raise_flag(flags, 0x4u);
+        return false;
+    }
+};
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity, 1u << 26); }
+
+// Byte offset of byte `col` of row `row` in a tile of 128-byte rows whose 16-byte chunks are permuted by XOR with
+// (row % 8): the 128-byte swizzle of TMA and of the matrix descriptors (tile base 1024-byte aligned).
+__device__ __forceinline__ uint32_t sw128_byte(int row, int col) {
+    return static_cast<uint32_t>(row * 128 + ((((col >> 4) ^ row) & 7) << 4) + (col & 15));
+}
+
+}  // namespace sm100
+}  // namespace kda
