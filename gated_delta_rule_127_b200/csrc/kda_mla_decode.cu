@@ -54,7 +54,9 @@ struct Shape {
     static constexpr int STAGES = E4M3 ? 4 : 2;
     static constexpr int QBUFS = !E4M3 && R == 32 ? 2 : 1;
     static constexpr int QBYTES = BLOCKS * NQ * 128 + R * 128;
-    static constexpr int PBYTES = NQ * 128;                // rows of 64 tokens (e4m3 uses half of each row)
+    static constexpr int PROW = E4M3 ? NQ : NQ * 2;        // weights: one row of all columns per token, 64 or 128 bytes
+    static constexpr int PBYTES = TOK * PROW;
+    static constexpr int PARTS = E4M3 ? 2 : R / 16;        // 16-byte pieces of a row per thread
     static constexpr int OFF_Q = STAGES * STAGE;
     static constexpr int OFF_P = OFF_Q + QBUFS * QBYTES;
     static constexpr int OFF_CTL = OFF_P + PBYTES;
@@ -72,10 +74,10 @@ struct Ctl {
     uint32_t bad[4];          // per stage: page slots of the tile with a bad page number
     long long scan[8];        // partial sums of the start search
     int b0, t0;
-    long long count, total;
+    long long first, count, total;
     alignas(16) float scale[E4M3 ? 4 : 1][TOK];  // e4m3: the tokens' scales, per stage
-    float qscale[E4M3 ? R : 1];                  // e4m3: the query rows' scales
-    float red[2][4][R];       // per tile parity, warp and row: maxima; at a segment's end sums
+    alignas(16) float qscale[E4M3 ? R : 4];      // e4m3: the query rows' scales
+    alignas(16) float red[4][R];          // per warp and row: maxima; at a segment's end sums
     alignas(16) float factor[R];                 // per row: rescaling factor; at a segment's end 1 / l
 };
 template <int R, bool E4M3>
@@ -95,22 +97,21 @@ __device__ __forceinline__ int cached_len(const MlaDecodeArgs& a, int b) {
 // Tiles of a sequence; an empty one still gets a tile, so that its rows are written.
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + TOK - 1) / TOK : 1; }
 
-// The workspace: for each CTA, which split sequence starts in it (sequence, last group; -1: none), and two
-// partial results (0: of a sequence begun in an earlier group, 1: of one begun here and left unfinished).
+// The workspace: two partial results per CTA (0: of a sequence begun in an earlier group, 1: of one begun here and
+// left unfinished), and for each of them its sequence (-1: none) and the first and last group that share it.
 struct Part {
-    int2* meta;   // [ctas]
+    int4* meta;   // [ctas][2]
     float* m;     // [ctas][2][R]
     float* l;     // [ctas][2][R]
     float* o;     // [ctas][2][R][512]
 };
 __host__ __device__ inline size_t part_bytes(int ctas, int R) {
-    return (static_cast<size_t>(ctas) * sizeof(int2) + 15) / 16 * 16 +
-           static_cast<size_t>(ctas) * 2 * R * (2 + kMlaLatent) * sizeof(float);
+    return static_cast<size_t>(ctas) * 2 * (sizeof(int4) + R * (2 + kMlaLatent) * sizeof(float));
 }
 __host__ __device__ inline Part part_of(void* ws, int ctas, int R) {
     Part p;
-    p.meta = static_cast<int2*>(ws);
-    p.o = reinterpret_cast<float*>(static_cast<char*>(ws) + (static_cast<size_t>(ctas) * sizeof(int2) + 15) / 16 * 16);
+    p.meta = static_cast<int4*>(ws);
+    p.o = reinterpret_cast<float*>(p.meta + static_cast<size_t>(ctas) * 2);
     p.m = p.o + static_cast<size_t>(ctas) * 2 * R * kMlaLatent;
     p.l = p.m + static_cast<size_t>(ctas) * 2 * R;
     return p;
@@ -152,6 +153,11 @@ __device__ __forceinline__ void reduce16(float (&v)[HH], int lane) {
             }
         }
     }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -201,16 +207,17 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 mbar_init(&c.kv_empty[i], 1);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&c.q_full[i], E4M3 ? 128 : 1);
+                mbar_init(&c.q_full[i], E4M3 ? 4 : 1);
                 mbar_init(&c.q_empty[i], 1);
                 mbar_init(&c.s_full[i], 1);
             }
-            mbar_init(&c.p_full, 128);
+            mbar_init(&c.p_full, 4);
             mbar_init(&c.pv_done, 1);
             mbar_init(&c.drain_bar, 1);
             fence_mbar_init();
         }
         if (warp == 5) tmem_alloc(&c.tmem, 512);
+        if (warp == 4 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_kv : lane == 1 ? &tm_pe : lane == 2 ? &tm_q : &tm_qp);
         __syncthreads();
         long long total = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
@@ -243,14 +250,20 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 c.count = before - at;
             }
         }
-        if (tid == 0) c.total = total;
+        if (tid == 0) {
+            c.first = first;
+            c.total = total;
+        }
         tc_fence_before_sync();
         __syncthreads();
         tc_fence_after_sync();
     }
+    // the joining kernel may be set up now; it waits for this one's end itself
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = c.tmem;
     const RoleWait wait{a.wait_polls, &c.abort_word, a.flags};
-    if (a.workspace && tid == 0) part_of(a.workspace, gridDim.x, R).meta[blockIdx.x] = make_int2(-1, -1);
+    if (a.workspace && tid == 0)
+        for (int i = 0; i < 2; ++i) part_of(a.workspace, gridDim.x, R).meta[blockIdx.x * 2 + i] = make_int4(-1, 0, 0, 0);
 
     if (c.count > 0) {
         Walk w;
@@ -325,90 +338,108 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
         } else if (warp == 5) {
             // ---------------------------------------------------------------- products
-            const uint32_t base = smem_u32(smem), qs = base + SH::OFF_Q, ps = base + SH::OFF_P;
+            // Two cursors over the tiles: scores (at most two ahead, one per score buffer) and second products.  Whatever
+            // is ready is issued, a second product first: it frees a stage, and must not wait behind scores whose
+            // tile is still on its way.
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+            const uint32_t qs = base + SH::OFF_Q, tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t ps = SH::PROW == 128 ? sw128_desc(base + SH::OFF_P, 16, 1024) : sw64_desc(base + SH::OFF_P, 16, 512);
             constexpr uint32_t idesc_s = E4M3 ? idesc_e4m3(64, SH::NQ, false, false) : idesc_bf16(64, R, false, false);
             constexpr uint32_t idesc_sp = idesc_bf16(64, R, false, false);
-            constexpr uint32_t idesc_o = E4M3 ? idesc_e4m3(128, SH::NQ, true, false) : idesc_bf16(128, R, true, false);
-            bool ok = true;
-            uint32_t seg = 0;
-            // scores of tile number g of the CTA (of segment sg); `last`: the segment's last tile
-            auto scores = [&](uint32_t g, uint32_t sg, bool first, bool last) -> bool {
-                const uint32_t st = g % SH::STAGES, qb = sg % SH::QBUFS;
-                if (first && !wait(&c.q_full[qb], (sg / SH::QBUFS) & 1)) return false;
-                if (!wait(&c.kv_full[st], (g / SH::STAGES) & 1)) return false;
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t kv = base + st * SH::STAGE, q = qs + qb * SH::QBYTES;
-                    const uint32_t d = tmem + (g & 1) * SH::S_COLS;
-#pragma unroll
-                    for (int k = 0; k < SH::BLOCKS; ++k)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint64_t da = sw128_desc(kv + k * SH::BLK + j * 32, 16, 1024);
-                            const uint64_t db = sw128_desc(q + k * SH::NQ * 128 + j * 32, 16, 1024);
-                            if (E4M3) mma_f8(d, da, db, idesc_s, k + j > 0);
-                            else mma_f16(d, da, db, idesc_s, k + j > 0);
-                        }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16(E4M3 ? d + SH::NQ : d, sw128_desc(kv + SH::BLOCKS * SH::BLK + j * 32, 16, 1024),
-                                sw128_desc(q + SH::BLOCKS * SH::NQ * 128 + j * 32, 16, 1024), idesc_sp,
-                                E4M3 ? j > 0 : 1);
-                    mma_commit(&c.s_full[g & 1]);
-                    if (last) mma_commit(&c.q_empty[qb]);
-                }
-                __syncwarp();
-                return true;
-            };
-            uint32_t g = 0;
-            bool issued = scores(0, 0, true, w.n == 1);
-            ok = issued;
-            while (ok) {
-                // the next tile's scores go first, so that its softmax overlaps this tile's second product; across
-                // segments only where the queries have a buffer of their own
-                bool more = true;
-                for (int i = 0; i < w.n && ok; ++i, ++g) {
-                    Walk nx = w;
-                    const bool inside = i + 1 < w.n;
-                    more = inside || nx.next(a);
-                    if (inside) ok = scores(g + 1, seg, false, i + 2 == w.n);
-                    else if (more && SH::QBUFS == 2) ok = scores(g + 1, seg + 1, true, nx.n == 1);
-                    if (!ok || !wait(&c.p_full, g & 1)) { ok = false; break; }
+            constexpr uint32_t idesc_o = E4M3 ? idesc_e4m3(128, SH::NQ, true, true) : idesc_bf16(128, R, true, true);
+            Walk ws = w;
+            int is = 0, ip = 0;               // tile within the segment
+            uint32_t gs = 0, gp = 0, seg = 0; // tile of the CTA; the scores' segment
+            bool more_s = true, ok = true;
+            WaitBudget budget;
+            uint32_t polls = 0;
+            while (true) {
+                if (gs > gp && wait.ready(&c.p_full, gp & 1)) {
                     tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint32_t st = g % SH::STAGES, kv = base + st * SH::STAGE;
+                    const uint32_t st = gp % SH::STAGES;
+                    const uint64_t v0 = sw128_desc(base + st * SH::STAGE, SH::BLK, 1024);
+                    if (elect_one()) {
 #pragma unroll
                         for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                             for (int k = 0; k < (E4M3 ? 2 : 4); ++k) {
-                                const uint32_t d = tmem + SH::COL_O + ch * SH::NQ;
-                                const uint64_t db = sw128_desc(ps + k * 32, 16, 1024);
+                                const uint32_t d = tm + SH::COL_O + ch * SH::NQ;
+                                const uint64_t pk = ps + ((k * (E4M3 ? 32 : 16) * SH::PROW) >> 4);
                                 if (E4M3)  // 32 tokens of 128 channels: four groups of 8 tokens, 1024 bytes each
-                                    mma_f8(d, sw128_desc(kv + ch * SH::BLK + k * 4096, SH::BLK, 1024), db, idesc_o,
-                                           i > 0 || k > 0);
+                                    mma_f8(d, v0 + ((ch * SH::BLK + k * 4096) >> 4), pk, idesc_o, ip > 0 || k > 0);
                                 else       // 16 tokens of 2 x 64 channels
-                                    mma_f16(d, sw128_desc(kv + 2 * ch * SH::BLK + k * 2048, SH::BLK, 1024), db, idesc_o,
-                                            i > 0 || k > 0);
+                                    mma_f16(d, v0 + ((2 * ch * SH::BLK + k * 2048) >> 4), pk, idesc_o,
+                                            ip > 0 || k > 0);
                             }
                         mma_commit(&c.kv_empty[st]);
                         mma_commit(&c.pv_done);
                     }
                     __syncwarp();
-                    if (!inside && more && SH::QBUFS == 1) ok = scores(g + 1, seg + 1, true, nx.n == 1);
+                    ++gp;
+                    if (++ip == w.n) {
+                        ip = 0;
+                        if (!w.next(a)) break;
+                    }
+                    budget = WaitBudget();
+                    polls = 0;
+                    continue;
                 }
-                ++seg;
-                if (!ok || !w.next(a)) break;
+                const uint32_t st = gs % SH::STAGES, qb = seg % SH::QBUFS;
+                if (more_s && gs - gp < 2 && wait.ready(&c.kv_full[st], (gs / SH::STAGES) & 1) &&
+                    (is > 0 || wait.ready(&c.q_full[qb], (seg / SH::QBUFS) & 1))) {
+                    tc_fence_after_sync();
+                    const uint32_t d = tm + (gs & 1) * SH::S_COLS;
+                    const uint64_t k0 = sw128_desc(base + st * SH::STAGE, 16, 1024);
+                    const uint64_t q0 = sw128_desc(qs + qb * SH::QBYTES, 16, 1024);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < SH::BLOCKS; ++k)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint64_t da = k0 + ((k * SH::BLK + j * 32) >> 4);
+                                const uint64_t db = q0 + ((k * SH::NQ * 128 + j * 32) >> 4);
+                                if (E4M3) mma_f8(d, da, db, idesc_s, k + j > 0);
+                                else mma_f16(d, da, db, idesc_s, k + j > 0);
+                            }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_f16(E4M3 ? d + SH::NQ : d, k0 + ((SH::BLOCKS * SH::BLK + j * 32) >> 4),
+                                    q0 + ((SH::BLOCKS * SH::NQ * 128 + j * 32) >> 4), idesc_sp, E4M3 ? j > 0 : 1);
+                        mma_commit(&c.s_full[gs & 1]);
+                        if (is + 1 == ws.n) mma_commit(&c.q_empty[qb]);
+                    }
+                    __syncwarp();
+                    ++gs;
+                    if (++is == ws.n) {
+                        is = 0;
+                        ++seg;
+                        more_s = ws.next(a);
+                    }
+                    budget = WaitBudget();
+                    polls = 0;
+                    continue;
+                }
+                if (__any_sync(0xffffffffu, polls++ >= a.wait_polls || ((polls & 15u) == 0 && wait.aborted()) ||
+                                                budget.expired())) {
+                    wait.give_up();
+                    ok = false;
+                    break;
+                }
             }
             if (!ok) {  // let issued products finish before the block ends
-                if (lane == 0) mma_commit(&c.drain_bar);
+                if (elect_one()) mma_commit(&c.drain_bar);
+                __syncwarp();
                 drain(&c.drain_bar, 0);
             }
         } else {
             // ---------------------------------------------------------------- softmax, rescaling, output
             const int tok = warp * 16 + (lane & 15), half = lane >> 4;
             const float sl2 = a.scale * 1.4426950408889634f;
+            constexpr float kOver = E4M3 ? 8.5f : 8.f, kBelow = E4M3 ? 4.f : 0.f;
             const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
             unsigned char* p_tile = smem + SH::OFF_P;
+            // this thread's first row: new token and head (rows past the sequence's own are never stored)
+            const int new0 = (row0 + half * HH) / a.H, head0 = (row0 + half * HH) % a.H;
             uint32_t g = 0;
             // ok: this warp's waits so far; stop: some warp's have failed, known to all four at the same barrier
             bool ok = true, stop = false;
@@ -420,30 +451,27 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const bool real = row0 + r < rows;
                 const int64_t row = static_cast<int64_t>(b) * rows + row0 + r;
                 uint4 v[16];
-                float m = 0.f;
-                bool finite = true;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    v[i] = real ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) +
-                                                                 row * kMlaLatent)[part + 4 * i]
+                    v[i] = real ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) +
+                                                                       row * kMlaLatent) + part + 4 * i)
                                 : make_uint4(0, 0, 0, 0);
                 uint4 pe[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    pe[i] = real ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_pe) +
-                                                                  row * kMlaPe)[2 * part + i]
+                    pe[i] = real ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_pe) +
+                                                                        row * kMlaPe) + 2 * part + i)
                                  : make_uint4(0, 0, 0, 0);
+                __nv_bfloat162 top = __nv_bfloat162(__float2bfloat16(0.f), __float2bfloat16(0.f));
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float lo = __uint_as_float(x[j] << 16), hi = __uint_as_float(x[j] & 0xFFFF0000u);
-                        finite = finite && isfinite(lo) && isfinite(hi);
-                        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[j])));
                 }
-                if (!finite) m = INFINITY;
+                const float t0 = __low2float(top), t1 = __high2float(top);
+                float m = isfinite(t0) && isfinite(t1) ? fmaxf(t0, t1) : INFINITY;
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 // the least k with m <= 448 2^k (448 = 1.75 * 2^8); a row that is not finite gives NaN scores
@@ -470,7 +498,8 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int i = 0; i < 2; ++i)
                     *reinterpret_cast<uint4*>(q + SH::BLOCKS * SH::NQ * 128 + sw128_byte(r, (2 * part + i) * 16)) = pe[i];
                 fence_async_smem();
-                mbar_arrive(&c.q_full[0]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.q_full[0]);
             };
             if (E4M3) {
                 load_queries(w.b);
@@ -483,27 +512,37 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int i = 0; i < HH; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
                 for (int t = 0; t < w.n; ++t, ++g) {
                     const uint32_t st = g % SH::STAGES;
-                    ok = ok && wait(&c.s_full[g & 1], (g >> 1) & 1) && wait(&c.kv_full[st], (g / SH::STAGES) & 1);
+                    ok = ok && wait(&c.kv_full[st], (g / SH::STAGES) & 1) && wait(&c.s_full[g & 1], (g >> 1) & 1);
                     tc_fence_after_sync();
                     float x[HH];
                     const uint32_t s_at = tmem + lane_base + (g & 1) * SH::S_COLS;
                     float ts = 1.f, ls = 0.f;   // the token's scale and its log2
                     const int pos = (w.t + t) * TOK + tok;
                     const uint32_t bads = c.bad[st];
-                    const bool seen = pos < w.len &&
-                                      !(bads >> (tok >> min(a.cache.page_shift, 6)) & 1u);
+                    const bool seen = pos < w.len && !(bads >> (tok >> min(a.cache.page_shift, 6)) & 1u);
                     if constexpr (E4M3) {
-                        float lo[HH], pe[HH];
-                        tmem_ld16_x2<HH>(s_at, x);
-                        tmem_ld16_x2<HH>(s_at + R, lo);
-                        tmem_ld16_x2<HH>(s_at + SH::NQ, pe);
+                        uint32_t hi[HH], lo[HH], pe[HH];
+                        tmem_ld16_x2_nw<HH>(s_at, hi);
+                        tmem_ld16_x2_nw<HH>(s_at + R, lo);
+                        tmem_ld16_x2_nw<HH>(s_at + SH::NQ, pe);
                         if (seen) {
                             ts = c.scale[st][tok];
-                            ls = log2f(ts);
+                            ls = __log2f(ts);
                         }
+                        tmem_ld_wait();
+                        after_ld_wait(hi);
+                        after_ld_wait(lo);
+                        after_ld_wait(pe);
+                        const float4* qs = reinterpret_cast<const float4*>(c.qscale + half * HH);
 #pragma unroll
-                        for (int i = 0; i < HH; ++i)
-                            x[i] = sl2 * fmaf((x[i] + 0.0625f * lo[i]) * ts, c.qscale[half * HH + i], pe[i]);
+                        for (int i = 0; i < HH; i += 4) {
+                            const float4 q4 = qs[i / 4];
+                            const float q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[i + j] = sl2 * fmaf(fmaf(0.0625f, __uint_as_float(lo[i + j]), __uint_as_float(hi[i + j])) * ts,
+                                                      q[j], __uint_as_float(pe[i + j]));
+                        }
                     } else {
                         if constexpr (R == 32) tmem_ld16_x2<HH>(s_at, x);
                         else tmem_ld32_x2<HH>(s_at, x);
@@ -512,10 +551,14 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                     const bool edge = (w.t + t + 1) * TOK > w.len - (a.S - 1) || bads != 0u;
                     if (edge) {
+                        int ends = w.len - (a.S - 1) + new0, head = head0;  // what row i sees ends there
 #pragma unroll
                         for (int i = 0; i < HH; ++i) {
-                            const int s = min((row0 + half * HH + i) / a.H, a.S - 1);
-                            if (!seen || pos >= w.len - (a.S - 1 - s)) x[i] = -INFINITY;
+                            if (!seen || pos >= ends) x[i] = -INFINITY;
+                            if (++head == a.H) {
+                                head = 0;
+                                ++ends;
+                            }
                         }
                         // rows of the tile that no query sees hold whatever lay there: zero them, so that their
                         // weight of 0 meets no NaN in the second product (the first one is done with them)
@@ -528,39 +571,46 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                         make_uint4(0, 0, 0, 0);
                         }
                     }
-                    // the tile's maximum of each row (e4m3: of x + log2 s)
-                    float v[HH];
+                    // Does some score exceed its row's reference by too much?  Seldom; only then are the tile's maxima
+                    // needed at all (e4m3: of x + log2 s).
+                    bool over = false;
 #pragma unroll
-                    for (int i = 0; i < HH; ++i) v[i] = x[i] + ls;
-                    reduce16<HH, true>(v, lane);
+                    for (int i = 0; i < HH; ++i) over = over || x[i] + ls > m[i] + kOver;
+                    // (a failed wait takes the same way, to the barrier at which all four warps stop)
+                    const bool move = group_sync_or(1, 128, over || !ok);
+                    if (move) {
+                        float v[HH];
 #pragma unroll
-                    for (int i = 0; i < HH / 16; ++i) c.red[g & 1][warp][half * HH + (lane & 15) * (HH / 16) + i] = v[i];
-                    stop = group_sync_or(1, 128, !ok);
-                    if (stop) break;
-                    constexpr float kOver = E4M3 ? 8.5f : 8.f, kBelow = E4M3 ? 4.f : 0.f;
-                    bool move = false;
-                    float top[HH];
+                        for (int i = 0; i < HH; ++i) v[i] = x[i] + ls;
+                        reduce16<HH, true>(v, lane);
 #pragma unroll
-                    for (int i = 0; i < HH; ++i) {
-                        const int h = half * HH + i;
-                        const auto& red = c.red[g & 1];
-                        top[i] = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
-                        move = move || top[i] > m[i] + kOver;
-                    }
-                    move = __any_sync(0xffffffffu, move);
-                    // this tile's weights overwrite the last one's, and the output moves: the last product must be done
-                    if (g > 0) ok = ok && wait(&c.pv_done, (g - 1) & 1);
-                    tc_fence_after_sync();
-                    if (move) {  // the same for all 128 threads: every warp has seen the same maxima
+                        for (int i = 0; i < HH / 16; ++i) c.red[warp][half * HH + (lane & 15) * (HH / 16) + i] = v[i];
+                        stop = group_sync_or(1, 128, !ok);
+                        if (stop) break;
+                        // the accumulated output moves too: the last product must be done with it
+                        if (g > 0) ok = ok && wait(&c.pv_done, (g - 1) & 1);
+                        tc_fence_after_sync();
 #pragma unroll
-                        for (int i = 0; i < HH; ++i) {
-                            float f = 1.f;
-                            if (top[i] > m[i] + kOver) {
-                                f = ex2(m[i] - (top[i] - kBelow));
-                                m[i] = top[i] - kBelow;
-                                l[i] *= f;
+                        for (int i = 0; i < HH; i += 4) {
+                            float4 r[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const float4*>(&c.red[k][half * HH + i]);
+                            const float top[4] = {fmaxf(fmaxf(r[0].x, r[1].x), fmaxf(r[2].x, r[3].x)),
+                                                  fmaxf(fmaxf(r[0].y, r[1].y), fmaxf(r[2].y, r[3].y)),
+                                                  fmaxf(fmaxf(r[0].z, r[1].z), fmaxf(r[2].z, r[3].z)),
+                                                  fmaxf(fmaxf(r[0].w, r[1].w), fmaxf(r[2].w, r[3].w))};
+                            float f[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                f[k] = 1.f;
+                                if (top[k] > m[i + k] + kOver) {
+                                    f[k] = ex2(m[i + k] - (top[k] - kBelow));
+                                    m[i + k] = top[k] - kBelow;
+                                    l[i + k] *= f[k];
+                                }
                             }
-                            if (tid == 0 || tid == 16) c.factor[half * HH + i] = f;
+                            if (tid == 0 || tid == 16)
+                                *reinterpret_cast<float4*>(c.factor + half * HH + i) = make_float4(f[0], f[1], f[2], f[3]);
                         }
                         group_sync(1, 128);
                         if (t > 0) {
@@ -580,36 +630,41 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             tmem_st_wait();
                         }
                     }
-                    // weights, into the second product's B operand [rows][64 tokens]
+                    // weights, one row of all columns per token (the second product's MN-major B operand): this thread
+                    // has HH neighbouring columns of its token, of each part
+                    uint4 pk[SH::PARTS];
+#pragma unroll
+                    for (int i = 0; i < HH; ++i) {
+                        x[i] = ex2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                        l[i] += x[i];
+                    }
                     if constexpr (E4M3) {
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int i = 0; i < HH; i += 2) {
-                            float e[2];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                e[j] = ex2(x[i + j] - (m[i + j] == -INFINITY ? 0.f : m[i + j]));
-                                l[i + j] += e[j];
-                            }
-                            uint32_t hi, lo;
-                            split_e4m3(e[0] * ts, e[1] * ts, hi, lo);
-                            const int r = half * HH + i;
-                            p_tile[sw128_byte(r, tok)] = static_cast<unsigned char>(hi);
-                            p_tile[sw128_byte(r + 1, tok)] = static_cast<unsigned char>(hi >> 8);
-                            p_tile[sw128_byte(R + r, tok)] = static_cast<unsigned char>(lo);
-                            p_tile[sw128_byte(R + r + 1, tok)] = static_cast<unsigned char>(lo >> 8);
-                        }
+                        for (int i = 0; i < 8; ++i) split_e4m3(x[2 * i] * ts, x[2 * i + 1] * ts, hi[i], lo[i]);
+                        pk[0] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+                        pk[1] = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < HH; ++i) {
-                            const float e = ex2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
-                            l[i] += e;
-                            *reinterpret_cast<__nv_bfloat16*>(p_tile + sw128_byte(half * HH + i, tok * 2)) = __float2bfloat16_rn(e);
-                        }
+                        for (int i = 0; i < SH::PARTS; ++i)
+                            pk[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                               pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                    }
+                    // they overwrite the last tile's: that product must be done
+                    if (g > 0) ok = ok && wait(&c.pv_done, (g - 1) & 1);
+#pragma unroll
+                    for (int i = 0; i < SH::PARTS; ++i) {
+                        const int chunk = E4M3 ? i * (R / 16) + half : half * SH::PARTS + i;  // 16-byte piece of the row
+                        *reinterpret_cast<uint4*>(p_tile + (SH::PROW == 128 ? sw128_byte(tok, chunk * 16)
+                                                                           : sw64_byte(tok, chunk * 16))) = pk[i];
                     }
                     fence_async_smem();
                     tc_fence_before_sync();
-                    mbar_arrive(&c.p_full);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.p_full);
                 }
+                if (stop) break;
+
                 if (stop) break;
 
                 // ---- the segment's end: sums over its tokens, then the output from tensor memory
@@ -617,9 +672,8 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const bool more = w.next(a);
                 if (E4M3 && more) load_queries(w.b);  // while the last product runs
                 reduce16<HH, false>(l, lane);
-                group_sync(1, 128);  // the last tile's maxima have been read by all
 #pragma unroll
-                for (int i = 0; i < HH / 16; ++i) c.red[0][warp][half * HH + (lane & 15) * (HH / 16) + i] = l[i];
+                for (int i = 0; i < HH / 16; ++i) c.red[warp][half * HH + (lane & 15) * (HH / 16) + i] = l[i];
                 ok = ok && wait(&c.pv_done, (g - 1) & 1);
                 tc_fence_after_sync();
                 if (tid == 0 || tid == 16) {
@@ -632,8 +686,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const Part part = part_of(a.workspace, gridDim.x, R);
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg_w.t == 0 ? 1 : 0);
                 if (tid < R) {
-                    const auto& red = c.red[0];
-                    const float sum = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+                    const float sum = (c.red[0][tid] + c.red[1][tid]) + (c.red[2][tid] + c.red[3][tid]);
                     const float mm = c.factor[tid];
                     const int r = row0 + tid;
                     if (whole) {
@@ -643,37 +696,64 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         part.m[slot * R + tid] = mm;
                         part.l[slot * R + tid] = sum;
                     }
-                    c.factor[tid] = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                    c.factor[tid] = sum == 0.f ? 0.f : 1.f / sum;
                 }
-                if (!whole && tid == 0 && seg_w.t == 0) {  // which groups share this sequence
-                    // its first tile is number `x - n + 1`..; the range of group k is [total k / G, total (k + 1) / G)
-                    const long long last = c.total * (group + 1) / groups - seg_w.n + seg_w.nt - 1;
-                    part.meta[blockIdx.x] = make_int2(seg_w.b, static_cast<int>(((last + 1) * groups - 1) / c.total));
+                if (!whole && tid == 0) {  // which groups share this sequence (group k's range begins at total k / G)
+                    const long long x = c.first + (seg_w.t == 0 ? c.count - seg_w.n : -seg_w.t);  // its first tile
+                    const auto group_of = [&](long long tile) { return static_cast<int>(((tile + 1) * groups - 1) / c.total); };
+                    part.meta[slot] = make_int4(seg_w.b, group_of(x), group_of(x + seg_w.nt - 1), 0);
                 }
                 group_sync(1, 128);
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-#pragma unroll 1
-                    for (int j = 0; j < R; j += 32) {
-                        float o[32];
-                        tmem_ld32(tmem + lane_base + SH::COL_O + k * SH::NQ + j, o);
-                        if (E4M3) {
-                            float lo[32];
-                            tmem_ld32(tmem + lane_base + SH::COL_O + k * SH::NQ + R + j, lo);
+                for (int k = 0; k < 4 * (R / 32); ++k) {  // 128 channels of 32 rows; thread = channel
+                    const int j = (k % (R / 32)) * 32, ch = k / (R / 32) * 128 + warp * 32 + lane;
+                    const uint32_t at = tmem + lane_base + SH::COL_O + k / (R / 32) * SH::NQ + j;
+                    uint32_t raw[32];
+                    float o[32];
+                    tmem_ld32_nw(at, raw);
+                    if constexpr (E4M3) {
+                        uint32_t lo[32];
+                        tmem_ld32_nw(at + R, lo);
+                        tmem_ld_wait();
+                        after_ld_wait(raw);
+                        after_ld_wait(lo);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = fmaf(0.0625f, lo[i], o[i]);
+                        for (int i = 0; i < 32; ++i) o[i] = fmaf(0.0625f, __uint_as_float(lo[i]), __uint_as_float(raw[i]));
+                    } else {
+                        tmem_ld_wait();
+                        after_ld_wait(raw);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
+                    }
+                    if (whole) {
+                        const float4* f = reinterpret_cast<const float4*>(c.factor + j);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 q = f[i];
+                            o[4 * i] *= q.x; o[4 * i + 1] *= q.y; o[4 * i + 2] *= q.z; o[4 * i + 3] *= q.w;
                         }
-                        const int ch = k * 128 + warp * 32 + lane;
-                        if (whole) {
-                            TO* out = static_cast<TO*>(a.o) + (static_cast<int64_t>(seg_w.b) * rows + row0 + j) * kMlaLatent + ch;
+                        const int have = rows - (row0 + j);  // rows of this sequence among the 32
+                        TO* out = static_cast<TO*>(a.o) + (static_cast<int64_t>(seg_w.b) * rows + row0 + j) * kMlaLatent;
+                        if constexpr (sizeof(TO) == 2) {
+                            // neighbouring lanes swap halves of their rows, so that a lane stores two channels at once:
+                            // an even lane those of rows 0-15, an odd one of rows 16-31
+                            const bool odd = lane & 1;
+                            out += (odd ? 16 * kMlaLatent : 0) + (ch & ~1);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 16], 1);
+                                const uint32_t v = odd ? pack_bf16(got, o[i + 16]) : pack_bf16(o[i], got);
+                                if (i + (odd ? 16 : 0) < have) *reinterpret_cast<uint32_t*>(out + i * kMlaLatent) = v;
+                            }
+                        } else {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (row0 + j + i < rows) out[i * kMlaLatent] = from_f32<TO>(o[i] * c.factor[j + i]);
-                        } else {
-                            float* out = part.o + (slot * R + j) * kMlaLatent + ch;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) out[i * kMlaLatent] = o[i];
+                                if (i < have) out[i * kMlaLatent + ch] = o[i];
                         }
+                    } else {
+                        float* out = part.o + (slot * R + j) * kMlaLatent + ch;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) out[i * kMlaLatent] = o[i];
                     }
                 }
                 tc_fence_before_sync();
@@ -690,50 +770,88 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
 }
 
-// Joins the partial results of the sequences that the cuts split: block = (CTA of the main kernel in which the
-// sequence starts, row), thread = 4 channels.  The parts are added in the order of their groups.
-template <typename TO>
-__global__ void __launch_bounds__(128) mla_combine_kernel(MlaDecodeArgs a, int R, int row_tiles, int ctas) {
+// Joins the partial results of the sequences that the cuts split.  Blocks: (CTA of the main kernel, 128 of the 512
+// channels); the n groups that share a sequence share its rows, n apart.  A warp adds up one row (a lane has 4 channels);
+// where a block has fewer rows than warps, several warps share a row's parts.  Every sum has a fixed order.  The grid is
+// launched while the main kernel runs and waits for its end.
+constexpr int COMBINE = 256;
+
+template <int R, typename TO>
+__global__ void __launch_bounds__(COMBINE) mla_combine_kernel(const __grid_constant__ MlaDecodeArgs a, int row_tiles,
+                                                              int ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int WARPS = COMBINE / 32, MOST = (GROUPS + 31) / 32;
+    __shared__ float wgt[GROUPS > 2 * R ? GROUPS : 2 * R];  // ceil(R / n) n for n <= GROUPS
+    __shared__ float4 acc[WARPS][32];
     const Part p = part_of(a.workspace, ctas, R);
-    const int cta = blockIdx.x, group = cta / row_tiles, rt = cta % row_tiles, i = blockIdx.y;
-    const int rows = a.S * a.H, r = rt * R + i;
-    if (r >= rows) return;
-    const int2 meta = p.meta[cta];
-    if (meta.x < 0) return;
-    const int n = meta.y - group + 1;
-    auto index = [&](int k) {  // row of part k
-        return ((static_cast<int64_t>(group + k) * row_tiles + rt) * 2 + (k == 0 ? 1 : 0)) * R + i;
-    };
-    __shared__ float wgt[GROUPS];
-    __shared__ float red[4];
-    const int tid = threadIdx.x;
-    float m = -INFINITY;
-    for (int k = tid; k < n; k += 128) m = fmaxf(m, p.m[index(k)]);
+    const int group = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, rows = min(a.S * a.H - rt * R, R);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = blockIdx.y * 128 + lane * 4;
+    for (int which = 0; which < 2; ++which) {
+        const int4 meta = p.meta[blockIdx.x * 2 + which];  // sequence, first and last group
+        if (meta.x < 0) continue;
+        const int n = meta.z - meta.y + 1, first = group - meta.y;
+        const int mine = first < rows ? (rows - first + n - 1) / n : 0;  // rows first, first + n, ...
+        const int64_t base = (static_cast<int64_t>(meta.y) * row_tiles + rt) * 2 * R;
+        auto index = [&](int k, int i) { return base + (static_cast<int64_t>(k) * row_tiles * 2 + (k == 0 ? 1 : 0)) * R + i; };
+        // weights 2^(m_k - m) / l of the block's rows, a warp per row, a lane per part
+        for (int x = warp; x < mine; x += WARPS) {
+            const int i = first + x * n;
+            float f[MOST], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    for (int k = tid; k < n; k += 128) {
-        const float mk = p.m[index(k)];
-        wgt[k] = mk == -INFINITY ? 0.f : ex2(mk - m);
+            for (int j = 0; j < MOST; ++j) {
+                const int k = j * 32 + lane;
+                f[j] = k < n ? p.m[index(k, i)] : -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < MOST; ++j) m = fmaxf(m, f[j]);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+            for (int j = 0; j < MOST; ++j) {
+                const int k = j * 32 + lane;
+                f[j] = f[j] == -INFINITY ? 0.f : ex2(f[j] - m);
+                if (k < n) l = fmaf(f[j], p.l[index(k, i)], l);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int j = 0; j < MOST; ++j)
+                if (j * 32 + lane < n) wgt[x * n + j * 32 + lane] = f[j] * inv;
+            if (a.lse && blockIdx.y == 0 && lane == 0)
+                a.lse[static_cast<int64_t>(meta.x) * a.S * a.H + rt * R + i] = (m + log2f(l)) * 0.6931471805599453f;
+        }
+        __syncthreads();
+        const int share = mine >= WARPS ? 1 : mine > 4 ? 1 : mine > 2 ? 2 : mine > 1 ? 4 : 8;  // warps per row
+        const int sub = warp % share;
+        for (int x0 = 0; x0 < mine; x0 += WARPS / share) {
+            const int x = x0 + warp / share, i = first + x * n;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < mine) {
+#pragma unroll 8
+                for (int k = sub; k < n; k += share) {
+                    const float g = wgt[x * n + k];
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o + index(k, i) * kMlaLatent + ch));
+                    o.x = fmaf(g, v.x, o.x); o.y = fmaf(g, v.y, o.y); o.z = fmaf(g, v.z, o.z); o.w = fmaf(g, v.w, o.w);
+                }
+            }
+            if (share > 1) {
+                acc[warp][lane] = o;
+                __syncthreads();
+                for (int k = 1; k < share && sub == 0; ++k) {
+                    const float4 v = acc[warp + k][lane];
+                    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                }
+                __syncthreads();
+            }
+            if (x < mine && sub == 0) {
+                TO* out = static_cast<TO*>(a.o) + (static_cast<int64_t>(meta.x) * a.S * a.H + rt * R + i) * kMlaLatent + ch;
+                if constexpr (sizeof(TO) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                else *reinterpret_cast<float4*>(out) = o;
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-        const float f = wgt[k];
-        const float4 v = *reinterpret_cast<const float4*>(p.o + index(k) * kMlaLatent + tid * 4);
-        l = fmaf(f, p.l[index(k)], l);
-        o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-    }
-    const int64_t row = static_cast<int64_t>(meta.x) * rows + r;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    TO* out = static_cast<TO*>(a.o) + row * kMlaLatent + tid * 4;
-    out[0] = from_f32<TO>(o.x * inv); out[1] = from_f32<TO>(o.y * inv);
-    out[2] = from_f32<TO>(o.z * inv); out[3] = from_f32<TO>(o.w * inv);
-    if (a.lse && tid == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // Query rows per CTA: 32, or 64 where a sequence has more rows than 32 and the cache is bf16 (the e4m3 form needs the
@@ -802,8 +920,16 @@ cudaError_t launch(const MlaDecodeArgs& a, const Grid& g) {
     kernel<<<ctas, THREADS, smem, a.stream>>>(q, qp, kv, pe, a, g.row_tiles, g.groups);
     err = cudaGetLastError();
     if (err != cudaSuccess || !a.workspace) return err;
-    mla_combine_kernel<TO><<<dim3(ctas, R), 128, 0, a.stream>>>(a, R, g.row_tiles, ctas);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas, kMlaLatent / 128);
+    cfg.blockDim = dim3(COMBINE);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mla_combine_kernel<R, TO>, a, g.row_tiles, ctas);
 }
 
 template <typename TO>

@@ -50,6 +50,58 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
         : "memory");
 }
 
+// Shared-memory matrix descriptor for 64-byte rows with the 64-byte swizzle (offsets as in sw128_desc).
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;  // version
+    d |= static_cast<uint64_t>(4) << 61;  // swizzle 64B
+    return d;
+}
+// Byte offset of byte `col` of row `row` in a tile of 64-byte rows whose 16-byte chunks are permuted by XOR with
+// (row / 2 % 4) (tile base 512-byte aligned).
+__device__ __forceinline__ uint32_t sw64_byte(int row, int col) {
+    return static_cast<uint32_t>(row * 64 + ((((col >> 4) ^ (row >> 1)) & 3) << 4) + (col & 15));
+}
+
+// 16 lanes read twice, as tmem_ld16_x2, without waiting.
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld16_x2_nw(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr), "n"(SPLIT));
+}
+
+// One lane of a converged warp.  Products issued under this predicate keep their descriptors in uniform registers:
+// 64 x 32 x 16 products measured 31 cycles apart, against 56 under a lane == 0 test.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0u;
+}
+
+// Whether phase `parity` has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Untiled copy into shared memory (16-byte aligned addresses and size), counted in bytes on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -67,16 +119,25 @@ struct RoleWait {
     unsigned int* flags;
 
     __device__ __forceinline__ bool aborted() const { return *abort_word != 0u; }
-    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        WaitBudget budget;
-        for (uint32_t i = 0; i < polls; ++i) {
-            if (mbar_poll(bar, parity)) return true;
-            if ((i & 7u) == 7u && aborted()) return false;
-            if (budget.expired()) break;
-        }
+    __device__ __forceinline__ void give_up() const {
         *abort_word = 1u;
         raise_flag(flags, 0x4u);
-        return false;
+    }
+    // Called by whole warps; the answer is the same for all lanes.
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        WaitBudget budget;
+        bool done = false;
+        for (uint32_t i = 0; i < polls; ++i) {
+            done = mbar_poll(bar, parity);
+            if (done || ((i & 7u) == 7u && aborted()) || budget.expired()) break;
+        }
+        done = __all_sync(0xffffffffu, done);
+        if (!done) give_up();
+        return done;
+    }
+    // One look without waiting, for a whole warp.
+    __device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, mbar_test(bar, parity));
     }
 };
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity, 1u << 26); }
