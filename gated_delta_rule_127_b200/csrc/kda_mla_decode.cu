@@ -25,8 +25,10 @@
 // sequence that a cut falls into leaves partial (m, l, O) in the workspace, which mla_combine_kernel joins in a
 // fixed order.  The cuts are found on the device from seq_lens, so a captured call follows new lengths.
 //
-// Roles of a CTA's 6 warps: 0-3 softmax, rescaling and output (thread = token, then channel), 4 loads (TMA), 5
-// issues the products.
+// Roles of a CTA's 11 warps: 0-3 and 4-7 softmax, rescaling and output, each group of four for half of the rows and
+// independent of the other (thread = token, then channel); 8 loads (TMA); 9 issues the first products, 10 the second
+// ones (issuing 16 to 36 of them takes as long as they run: one warp for both would keep a tile's finished weights
+// waiting behind the next tile's scores).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -41,7 +43,7 @@ namespace {
 using namespace sm100;
 
 constexpr int TOK = 64;          // tokens per tile
-constexpr int THREADS = 192;
+constexpr int THREADS = 352;
 constexpr int GROUPS = 148;      // CTAs the work is cut for (one per SM)
 constexpr int kSmemMax = 227 * 1024;
 
@@ -56,7 +58,6 @@ struct Shape {
     static constexpr int QBYTES = BLOCKS * NQ * 128 + R * 128;
     static constexpr int PROW = E4M3 ? NQ : NQ * 2;        // weights: one row of all columns per token, 64 or 128 bytes
     static constexpr int PBYTES = TOK * PROW;
-    static constexpr int PARTS = E4M3 ? 2 : R / 16;        // 16-byte pieces of a row per thread
     static constexpr int OFF_Q = STAGES * STAGE;
     static constexpr int OFF_P = OFF_Q + QBUFS * QBYTES;
     static constexpr int OFF_CTL = OFF_P + PBYTES;
@@ -68,11 +69,11 @@ struct Shape {
 
 template <int R, bool E4M3>
 struct Ctl {
-    uint64_t kv_full[4], kv_empty[4], q_full[2], q_empty[2], s_full[2], p_full, pv_done, drain_bar;
+    uint64_t kv_full[4], kv_empty[4], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full, pv_done, drain_bar[2];
     uint32_t tmem;
     uint32_t abort_word;
     uint32_t bad[4];          // per stage: page slots of the tile with a bad page number
-    long long scan[8];        // partial sums of the start search
+    long long scan[THREADS / 32];  // partial sums of the start search
     int b0, t0;
     long long first, count, total;
     alignas(16) float scale[E4M3 ? 4 : 1][TOK];  // e4m3: the tokens' scales, per stage
@@ -137,13 +138,17 @@ struct Walk {
     }
 };
 
-// Transposed reduction over the 16 lanes of a half warp: on return v[0 .. HH/16) hold the results of heads
-// (lane % 16) * (HH / 16) + i, each lane having kept half of its values at every step.
+// Transposed reduction over the 16 lanes of a half warp, each lane keeping half of its values at every step: on return
+// v[i] is the result of row (lane % 16) * HH / 16 + i (HH = 8: two lanes have the same row).
 template <int HH, bool MAX>
 __device__ __forceinline__ void reduce16(float (&v)[HH], int lane) {
 #pragma unroll
     for (int d = 8, n = HH / 2; d > 0; d >>= 1, n >>= 1) {
         const bool up = (lane & d) != 0;
+        if (n == 0) {
+            const float got = __shfl_xor_sync(0xffffffffu, v[0], d);
+            v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+        }
 #pragma unroll
         for (int i = 0; i < HH / 2; ++i) {
             if (i < n) {
@@ -179,7 +184,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_pe,
                   const __grid_constant__ MlaDecodeArgs a, int row_tiles, int groups) {
     using SH = Shape<R, E4M3>;
-    constexpr int HH = R / 2;
+    constexpr int HH = R / 4;  // rows per softmax thread
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctl<R, E4M3>& c = *reinterpret_cast<Ctl<R, E4M3>*>(smem + SH::OFF_CTL);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -207,17 +212,19 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 mbar_init(&c.kv_empty[i], 1);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&c.q_full[i], E4M3 ? 4 : 1);
+                mbar_init(&c.q_full[i], E4M3 ? 8 : 1);
                 mbar_init(&c.q_empty[i], 1);
                 mbar_init(&c.s_full[i], 1);
+                mbar_init(&c.s_empty[i], 8);
             }
-            mbar_init(&c.p_full, 4);
+            mbar_init(&c.p_full, 8);
             mbar_init(&c.pv_done, 1);
-            mbar_init(&c.drain_bar, 1);
+            mbar_init(&c.drain_bar[0], 1);
+            mbar_init(&c.drain_bar[1], 1);
             fence_mbar_init();
         }
-        if (warp == 5) tmem_alloc(&c.tmem, 512);
-        if (warp == 4 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_kv : lane == 1 ? &tm_pe : lane == 2 ? &tm_q : &tm_qp);
+        if (warp == 9) tmem_alloc(&c.tmem, 512);
+        if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_kv : lane == 1 ? &tm_pe : lane == 2 ? &tm_q : &tm_qp);
         __syncthreads();
         long long total = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
@@ -272,7 +279,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         w.left = c.count;
         w.open(a);
 
-        if (warp == 4) {
+        if (warp == 8) {
             // ---------------------------------------------------------------- loads
             const int shift = min(a.cache.page_shift, 6), prow = 1 << shift;     // tokens per box
             const int boxes = TOK >> shift;                                       // page slots of a tile
@@ -336,59 +343,23 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (uint32_t i = queries > SH::QBUFS ? queries - SH::QBUFS : 0; i < queries; ++i)
                     drain(&c.q_full[i % SH::QBUFS], (i / SH::QBUFS) & 1);
             }
-        } else if (warp == 5) {
-            // ---------------------------------------------------------------- products
-            // Two cursors over the tiles: scores (at most two ahead, one per score buffer) and second products.  Whatever
-            // is ready is issued, a second product first: it frees a stage, and must not wait behind scores whose
-            // tile is still on its way.
-            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-            const uint32_t qs = base + SH::OFF_Q, tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint64_t ps = SH::PROW == 128 ? sw128_desc(base + SH::OFF_P, 16, 1024) : sw64_desc(base + SH::OFF_P, 16, 512);
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- first products: scores
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), qs = base + SH::OFF_Q;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             constexpr uint32_t idesc_s = E4M3 ? idesc_e4m3(64, SH::NQ, false, false) : idesc_bf16(64, R, false, false);
-            constexpr uint32_t idesc_sp = idesc_bf16(64, R, false, false);
-            constexpr uint32_t idesc_o = E4M3 ? idesc_e4m3(128, SH::NQ, true, true) : idesc_bf16(128, R, true, true);
-            Walk ws = w;
-            int is = 0, ip = 0;               // tile within the segment
-            uint32_t gs = 0, gp = 0, seg = 0; // tile of the CTA; the scores' segment
-            bool more_s = true, ok = true;
-            WaitBudget budget;
-            uint32_t polls = 0;
-            while (true) {
-                if (gs > gp && wait.ready(&c.p_full, gp & 1)) {
+            constexpr uint32_t idesc_p = idesc_bf16(64, R, false, false);
+            uint32_t g = 0, seg = 0;
+            bool ok = true;
+            do {
+                const uint32_t qb = seg % SH::QBUFS;
+                ok = wait(&c.q_full[qb], (seg / SH::QBUFS) & 1);
+                for (int i = 0; i < w.n && ok; ++i) {
+                    const uint32_t st = g % SH::STAGES;
+                    ok = wait(&c.s_empty[g & 1], ((g >> 1) & 1) ^ 1) && wait(&c.kv_full[st], (g / SH::STAGES) & 1);
+                    if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t st = gp % SH::STAGES;
-                    const uint64_t v0 = sw128_desc(base + st * SH::STAGE, SH::BLK, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                            for (int k = 0; k < (E4M3 ? 2 : 4); ++k) {
-                                const uint32_t d = tm + SH::COL_O + ch * SH::NQ;
-                                const uint64_t pk = ps + ((k * (E4M3 ? 32 : 16) * SH::PROW) >> 4);
-                                if (E4M3)  // 32 tokens of 128 channels: four groups of 8 tokens, 1024 bytes each
-                                    mma_f8(d, v0 + ((ch * SH::BLK + k * 4096) >> 4), pk, idesc_o, ip > 0 || k > 0);
-                                else       // 16 tokens of 2 x 64 channels
-                                    mma_f16(d, v0 + ((2 * ch * SH::BLK + k * 2048) >> 4), pk, idesc_o,
-                                            ip > 0 || k > 0);
-                            }
-                        mma_commit(&c.kv_empty[st]);
-                        mma_commit(&c.pv_done);
-                    }
-                    __syncwarp();
-                    ++gp;
-                    if (++ip == w.n) {
-                        ip = 0;
-                        if (!w.next(a)) break;
-                    }
-                    budget = WaitBudget();
-                    polls = 0;
-                    continue;
-                }
-                const uint32_t st = gs % SH::STAGES, qb = seg % SH::QBUFS;
-                if (more_s && gs - gp < 2 && wait.ready(&c.kv_full[st], (gs / SH::STAGES) & 1) &&
-                    (is > 0 || wait.ready(&c.q_full[qb], (seg / SH::QBUFS) & 1))) {
-                    tc_fence_after_sync();
-                    const uint32_t d = tm + (gs & 1) * SH::S_COLS;
+                    const uint32_t d = tm + (g & 1) * SH::S_COLS;
                     const uint64_t k0 = sw128_desc(base + st * SH::STAGE, 16, 1024);
                     const uint64_t q0 = sw128_desc(qs + qb * SH::QBYTES, 16, 1024);
                     if (elect_one()) {
@@ -404,67 +375,94 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             mma_f16(E4M3 ? d + SH::NQ : d, k0 + ((SH::BLOCKS * SH::BLK + j * 32) >> 4),
-                                    q0 + ((SH::BLOCKS * SH::NQ * 128 + j * 32) >> 4), idesc_sp, E4M3 ? j > 0 : 1);
-                        mma_commit(&c.s_full[gs & 1]);
-                        if (is + 1 == ws.n) mma_commit(&c.q_empty[qb]);
+                                    q0 + ((SH::BLOCKS * SH::NQ * 128 + j * 32) >> 4), idesc_p, E4M3 ? j > 0 : 1);
+                        mma_commit(&c.s_full[g & 1]);
+                        if (i + 1 == w.n) mma_commit(&c.q_empty[qb]);
                     }
                     __syncwarp();
-                    ++gs;
-                    if (++is == ws.n) {
-                        is = 0;
-                        ++seg;
-                        more_s = ws.next(a);
-                    }
-                    budget = WaitBudget();
-                    polls = 0;
-                    continue;
+                    ++g;
                 }
-                if (__any_sync(0xffffffffu, polls++ >= a.wait_polls || ((polls & 15u) == 0 && wait.aborted()) ||
-                                                budget.expired())) {
-                    wait.give_up();
-                    ok = false;
-                    break;
-                }
-            }
+                ++seg;
+            } while (ok && w.next(a));
             if (!ok) {  // let issued products finish before the block ends
-                if (elect_one()) mma_commit(&c.drain_bar);
+                if (elect_one()) mma_commit(&c.drain_bar[0]);
                 __syncwarp();
-                drain(&c.drain_bar, 0);
+                drain(&c.drain_bar[0], 0);
+            }
+        } else if (warp == 10) {
+            // ---------------------------------------------------------------- second products: weighted latents
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t ps = SH::PROW == 128 ? sw128_desc(base + SH::OFF_P, 16, 1024) : sw64_desc(base + SH::OFF_P, 16, 512);
+            constexpr uint32_t idesc_o = E4M3 ? idesc_e4m3(128, SH::NQ, true, true) : idesc_bf16(128, R, true, true);
+            uint32_t g = 0;
+            bool ok = true;
+            do {
+                for (int i = 0; i < w.n; ++i) {
+                    ok = wait(&c.p_full, g & 1);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t st = g % SH::STAGES;
+                    const uint64_t v0 = sw128_desc(base + st * SH::STAGE, SH::BLK, 1024);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                            for (int k = 0; k < (E4M3 ? 2 : 4); ++k) {
+                                const uint32_t d = tm + SH::COL_O + ch * SH::NQ;
+                                const uint64_t pk = ps + ((k * (E4M3 ? 32 : 16) * SH::PROW) >> 4);
+                                if (E4M3)  // 32 tokens of 128 channels: four groups of 8 tokens, 1024 bytes each
+                                    mma_f8(d, v0 + ((ch * SH::BLK + k * 4096) >> 4), pk, idesc_o, i > 0 || k > 0);
+                                else       // 16 tokens of 2 x 64 channels
+                                    mma_f16(d, v0 + ((2 * ch * SH::BLK + k * 2048) >> 4), pk, idesc_o, i > 0 || k > 0);
+                            }
+                        mma_commit(&c.kv_empty[st]);
+                        mma_commit(&c.pv_done);
+                    }
+                    __syncwarp();
+                    ++g;
+                }
+            } while (ok && w.next(a));
+            if (!ok) {
+                if (elect_one()) mma_commit(&c.drain_bar[1]);
+                __syncwarp();
+                drain(&c.drain_bar[1], 0);
             }
         } else {
             // ---------------------------------------------------------------- softmax, rescaling, output
-            const int tok = warp * 16 + (lane & 15), half = lane >> 4;
+            // a warp reads the accumulators' lanes 32 (warp % 4) ..; of a score tile's 64 tokens that is 16, so its halves
+            // take a quarter of the rows each
+            const int wg = warp >> 2, sub = warp & 3, tok = sub * 16 + (lane & 15), half = lane >> 4;
+            const int bar = 1 + wg, h0 = wg * (R / 2) + half * HH;  // named barrier, first row of this thread
+            const bool writer = sub == 0 && (lane & 15) == 0;
             const float sl2 = a.scale * 1.4426950408889634f;
             constexpr float kOver = E4M3 ? 8.5f : 8.f, kBelow = E4M3 ? 4.f : 0.f;
-            const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+            const uint32_t lane_base = static_cast<uint32_t>(sub * 32) << 16;
             unsigned char* p_tile = smem + SH::OFF_P;
             // this thread's first row: new token and head (rows past the sequence's own are never stored)
-            const int new0 = (row0 + half * HH) / a.H, head0 = (row0 + half * HH) % a.H;
+            const int new0 = (row0 + h0) / a.H, head0 = (row0 + h0) % a.H;
             uint32_t g = 0;
             // ok: this warp's waits so far; stop: some warp's have failed, known to all four at the same barrier
             bool ok = true, stop = false;
 
-            // e4m3: a segment's queries as two e4m3 parts with a power-of-two scale per row; thread = (row, quarter)
+            // e4m3: a segment's queries as two e4m3 parts with a power-of-two scale per row; thread = (row, eighth)
             auto load_queries = [&](int b) {
-                const int r = tid >> 2, part = tid & 3;
+                const int r = tid >> 3, part = tid & 7;
                 unsigned char* q = smem + SH::OFF_Q;
                 const bool real = row0 + r < rows;
                 const int64_t row = static_cast<int64_t>(b) * rows + row0 + r;
-                uint4 v[16];
+                uint4 v[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8; ++i)
                     v[i] = real ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) +
-                                                                       row * kMlaLatent) + part + 4 * i)
+                                                                       row * kMlaLatent) + part + 8 * i)
                                 : make_uint4(0, 0, 0, 0);
-                uint4 pe[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    pe[i] = real ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_pe) +
-                                                                        row * kMlaPe) + 2 * part + i)
-                                 : make_uint4(0, 0, 0, 0);
+                const uint4 pe = real ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_pe) +
+                                                                             row * kMlaPe) + part)
+                                      : make_uint4(0, 0, 0, 0);
                 __nv_bfloat162 top = __nv_bfloat162(__float2bfloat16(0.f), __float2bfloat16(0.f));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -474,6 +472,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 float m = isfinite(t0) && isfinite(t1) ? fmaxf(t0, t1) : INFINITY;
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                 // the least k with m <= 448 2^k (448 = 1.75 * 2^8); a row that is not finite gives NaN scores
                 const uint32_t bits = __float_as_uint(m);
                 int k = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7FFFFFu) > 0x600000u ? 7 : 8);
@@ -483,48 +482,50 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     c.qscale[r] = m == INFINITY ? __uint_as_float(0x7FC00000u)
                                                 : __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t h[4], l[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         split_e4m3(__uint_as_float(x[j] << 16) * inv, __uint_as_float(x[j] & 0xFFFF0000u) * inv, h[j], l[j]);
-                    const int ch = (part + 4 * i) * 8;  // first of 8 channels
+                    const int ch = (part + 8 * i) * 8;  // first of 8 channels
                     unsigned char* blk = q + (ch >> 7) * SH::NQ * 128;
                     *reinterpret_cast<uint2*>(blk + sw128_byte(r, ch & 127)) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
                     *reinterpret_cast<uint2*>(blk + sw128_byte(R + r, ch & 127)) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4*>(q + SH::BLOCKS * SH::NQ * 128 + sw128_byte(r, (2 * part + i) * 16)) = pe[i];
+                *reinterpret_cast<uint4*>(q + SH::BLOCKS * SH::NQ * 128 + sw128_byte(r, part * 16)) = pe;
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.q_full[0]);
             };
             if (E4M3) {
                 load_queries(w.b);
-                group_sync(1, 128);
+                group_sync(bar, 128);
             }
 
             while (true) {
                 float m[HH], l[HH];
 #pragma unroll
                 for (int i = 0; i < HH; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+                if (E4M3 && w.left > w.n && row0 + (tid >> 3) < rows)  // the next segment's queries, into L2
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        static_cast<const __nv_bfloat16*>(a.q_latent) +
+                        (static_cast<int64_t>(w.b + 1) * rows + row0 + (tid >> 3)) * kMlaLatent + (tid & 7) * 64));
                 for (int t = 0; t < w.n; ++t, ++g) {
                     const uint32_t st = g % SH::STAGES;
                     ok = ok && wait(&c.kv_full[st], (g / SH::STAGES) & 1) && wait(&c.s_full[g & 1], (g >> 1) & 1);
                     tc_fence_after_sync();
                     float x[HH];
-                    const uint32_t s_at = tmem + lane_base + (g & 1) * SH::S_COLS;
+                    const uint32_t s_at = tmem + lane_base + (g & 1) * SH::S_COLS + wg * (R / 2);
                     float ts = 1.f, ls = 0.f;   // the token's scale and its log2
                     const int pos = (w.t + t) * TOK + tok;
                     const uint32_t bads = c.bad[st];
                     const bool seen = pos < w.len && !(bads >> (tok >> min(a.cache.page_shift, 6)) & 1u);
                     if constexpr (E4M3) {
                         uint32_t hi[HH], lo[HH], pe[HH];
-                        tmem_ld16_x2_nw<HH>(s_at, hi);
-                        tmem_ld16_x2_nw<HH>(s_at + R, lo);
-                        tmem_ld16_x2_nw<HH>(s_at + SH::NQ, pe);
+                        tmem_ld8_x2_nw<HH>(s_at, hi);
+                        tmem_ld8_x2_nw<HH>(s_at + R, lo);
+                        tmem_ld8_x2_nw<HH>(s_at + SH::NQ, pe);
                         if (seen) {
                             ts = c.scale[st][tok];
                             ls = __log2f(ts);
@@ -533,7 +534,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         after_ld_wait(hi);
                         after_ld_wait(lo);
                         after_ld_wait(pe);
-                        const float4* qs = reinterpret_cast<const float4*>(c.qscale + half * HH);
+                        const float4* qs = reinterpret_cast<const float4*>(c.qscale + h0);
 #pragma unroll
                         for (int i = 0; i < HH; i += 4) {
                             const float4 q4 = qs[i / 4];
@@ -544,11 +545,17 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                                       q[j], __uint_as_float(pe[i + j]));
                         }
                     } else {
-                        if constexpr (R == 32) tmem_ld16_x2<HH>(s_at, x);
-                        else tmem_ld32_x2<HH>(s_at, x);
+                        uint32_t raw[HH];
+                        if constexpr (R == 32) tmem_ld8_x2_nw<HH>(s_at, raw);
+                        else tmem_ld16_x2_nw<HH>(s_at, raw);
+                        tmem_ld_wait();
+                        after_ld_wait(raw);
 #pragma unroll
-                        for (int i = 0; i < HH; ++i) x[i] *= sl2;
+                        for (int i = 0; i < HH; ++i) x[i] = sl2 * __uint_as_float(raw[i]);
                     }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.s_empty[g & 1]);
                     const bool edge = (w.t + t + 1) * TOK > w.len - (a.S - 1) || bads != 0u;
                     if (edge) {
                         int ends = w.len - (a.S - 1) + new0, head = head0;  // what row i sees ends there
@@ -564,7 +571,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         // weight of 0 meets no NaN in the second product (the first one is done with them)
                         if (!seen && half == 0) {
 #pragma unroll 1
-                            for (int k = 0; k < SH::BLOCKS; ++k)
+                            for (int k = wg; k < SH::BLOCKS; k += 2)
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
                                     *reinterpret_cast<uint4*>(smem + st * SH::STAGE + k * SH::BLK + tok * 128 + j * 16) =
@@ -577,15 +584,15 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < HH; ++i) over = over || x[i] + ls > m[i] + kOver;
                     // (a failed wait takes the same way, to the barrier at which all four warps stop)
-                    const bool move = group_sync_or(1, 128, over || !ok);
+                    const bool move = group_sync_or(bar, 128, over || !ok);
                     if (move) {
                         float v[HH];
 #pragma unroll
                         for (int i = 0; i < HH; ++i) v[i] = x[i] + ls;
                         reduce16<HH, true>(v, lane);
 #pragma unroll
-                        for (int i = 0; i < HH / 16; ++i) c.red[warp][half * HH + (lane & 15) * (HH / 16) + i] = v[i];
-                        stop = group_sync_or(1, 128, !ok);
+                        for (int i = 0; i < (HH + 15) / 16; ++i) c.red[sub][h0 + (lane & 15) * HH / 16 + i] = v[i];
+                        stop = group_sync_or(bar, 128, !ok);
                         if (stop) break;
                         // the accumulated output moves too: the last product must be done with it
                         if (g > 0) ok = ok && wait(&c.pv_done, (g - 1) & 1);
@@ -594,7 +601,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         for (int i = 0; i < HH; i += 4) {
                             float4 r[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const float4*>(&c.red[k][half * HH + i]);
+                            for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const float4*>(&c.red[k][h0 + i]);
                             const float top[4] = {fmaxf(fmaxf(r[0].x, r[1].x), fmaxf(r[2].x, r[3].x)),
                                                   fmaxf(fmaxf(r[0].y, r[1].y), fmaxf(r[2].y, r[3].y)),
                                                   fmaxf(fmaxf(r[0].z, r[1].z), fmaxf(r[2].z, r[3].z)),
@@ -609,54 +616,61 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                     l[i + k] *= f[k];
                                 }
                             }
-                            if (tid == 0 || tid == 16)
-                                *reinterpret_cast<float4*>(c.factor + half * HH + i) = make_float4(f[0], f[1], f[2], f[3]);
+                            if (writer)
+                                *reinterpret_cast<float4*>(c.factor + h0 + i) = make_float4(f[0], f[1], f[2], f[3]);
                         }
-                        group_sync(1, 128);
+                        group_sync(bar, 128);
                         if (t > 0) {
 #pragma unroll 1
-                            for (int k = 0; k < 4 * SH::NQ / 32; ++k) {
-                                float o[32];
-                                const uint32_t at = tmem + lane_base + SH::COL_O + k * 32;
-                                tmem_ld32(at, o);
-                                const float4* f = reinterpret_cast<const float4*>(c.factor + (k * 32) % R);
+                            for (int k = 0; k < 4 * SH::NQ / R; ++k) {  // chunk and part: this group's half of the rows
+                                float o[R / 2];
+                                const uint32_t at = tmem + lane_base + SH::COL_O + k * R + wg * (R / 2);
+                                if constexpr (R == 32) tmem_ld16(at, o);
+                                else tmem_ld32(at, o);
+                                const float4* f = reinterpret_cast<const float4*>(c.factor + wg * (R / 2));
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
+                                for (int i = 0; i < R / 8; ++i) {
                                     const float4 q = f[i];
                                     o[4 * i] *= q.x; o[4 * i + 1] *= q.y; o[4 * i + 2] *= q.z; o[4 * i + 3] *= q.w;
                                 }
-                                tmem_st32(at, o);
+                                if constexpr (R == 32) tmem_st16(at, o);
+                                else tmem_st32(at, o);
                             }
                             tmem_st_wait();
                         }
                     }
                     // weights, one row of all columns per token (the second product's MN-major B operand): this thread
                     // has HH neighbouring columns of its token, of each part
-                    uint4 pk[SH::PARTS];
 #pragma unroll
                     for (int i = 0; i < HH; ++i) {
                         x[i] = ex2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
                         l[i] += x[i];
                     }
+                    uint32_t pk[HH / 2];  // bf16: pairs of columns; e4m3: pairs of the high parts, then of the low ones
                     if constexpr (E4M3) {
-                        uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) split_e4m3(x[2 * i] * ts, x[2 * i + 1] * ts, hi[i], lo[i]);
-                        pk[0] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-                        pk[1] = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+                        for (int i = 0; i < HH / 4; ++i) {
+                            uint32_t h[2], lo[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) split_e4m3(x[4 * i + 2 * j] * ts, x[4 * i + 2 * j + 1] * ts, h[j], lo[j]);
+                            pk[i] = h[0] | h[1] << 16;
+                            pk[HH / 4 + i] = lo[0] | lo[1] << 16;
+                        }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < SH::PARTS; ++i)
-                            pk[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                               pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                        for (int i = 0; i < HH / 2; ++i) pk[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
                     }
                     // they overwrite the last tile's: that product must be done
                     if (g > 0) ok = ok && wait(&c.pv_done, (g - 1) & 1);
+                    if constexpr (E4M3) {
+                        *reinterpret_cast<uint2*>(p_tile + sw64_byte(tok, h0)) = make_uint2(pk[0], pk[1]);
+                        *reinterpret_cast<uint2*>(p_tile + sw64_byte(tok, R + h0)) = make_uint2(pk[2], pk[3]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < SH::PARTS; ++i) {
-                        const int chunk = E4M3 ? i * (R / 16) + half : half * SH::PARTS + i;  // 16-byte piece of the row
-                        *reinterpret_cast<uint4*>(p_tile + (SH::PROW == 128 ? sw128_byte(tok, chunk * 16)
-                                                                           : sw64_byte(tok, chunk * 16))) = pk[i];
+                        for (int i = 0; i < HH / 8; ++i)
+                            *reinterpret_cast<uint4*>(p_tile + (SH::PROW == 128 ? sw128_byte(tok, h0 * 2 + i * 16)
+                                                                               : sw64_byte(tok, h0 * 2 + i * 16))) =
+                                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                     }
                     fence_async_smem();
                     tc_fence_before_sync();
@@ -673,182 +687,196 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (E4M3 && more) load_queries(w.b);  // while the last product runs
                 reduce16<HH, false>(l, lane);
 #pragma unroll
-                for (int i = 0; i < HH / 16; ++i) c.red[warp][half * HH + (lane & 15) * (HH / 16) + i] = l[i];
+                for (int i = 0; i < (HH + 15) / 16; ++i) c.red[sub][h0 + (lane & 15) * HH / 16 + i] = l[i];
                 ok = ok && wait(&c.pv_done, (g - 1) & 1);
                 tc_fence_after_sync();
-                if (tid == 0 || tid == 16) {
+                if (writer) {
 #pragma unroll
-                    for (int i = 0; i < HH; ++i) c.factor[half * HH + i] = m[i];
+                    for (int i = 0; i < HH; ++i) c.factor[h0 + i] = m[i];
                 }
-                stop = group_sync_or(1, 128, !ok);
+                stop = group_sync_or(bar, 128, !ok);
                 if (stop) break;
                 const bool whole = seg_w.n == seg_w.nt;
                 const Part part = part_of(a.workspace, gridDim.x, R);
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg_w.t == 0 ? 1 : 0);
-                if (tid < R) {
-                    const float sum = (c.red[0][tid] + c.red[1][tid]) + (c.red[2][tid] + c.red[3][tid]);
-                    const float mm = c.factor[tid];
-                    const int r = row0 + tid;
+                if ((tid & 127) < R / 2) {
+                    const int h = wg * (R / 2) + (tid & 127), r = row0 + h;
+                    const float sum = (c.red[0][h] + c.red[1][h]) + (c.red[2][h] + c.red[3][h]), mm = c.factor[h];
                     if (whole) {
                         if (a.lse && r < rows)
                             a.lse[static_cast<int64_t>(seg_w.b) * rows + r] = (mm + log2f(sum)) * 0.6931471805599453f;
                     } else {
-                        part.m[slot * R + tid] = mm;
-                        part.l[slot * R + tid] = sum;
+                        part.m[slot * R + h] = mm;
+                        part.l[slot * R + h] = sum;
                     }
-                    c.factor[tid] = sum == 0.f ? 0.f : 1.f / sum;
+                    c.factor[h] = sum == 0.f ? 0.f : 1.f / sum;
                 }
                 if (!whole && tid == 0) {  // which groups share this sequence (group k's range begins at total k / G)
                     const long long x = c.first + (seg_w.t == 0 ? c.count - seg_w.n : -seg_w.t);  // its first tile
                     const auto group_of = [&](long long tile) { return static_cast<int>(((tile + 1) * groups - 1) / c.total); };
                     part.meta[slot] = make_int4(seg_w.b, group_of(x), group_of(x + seg_w.nt - 1), 0);
                 }
-                group_sync(1, 128);
+                group_sync(bar, 128);
 #pragma unroll 1
-                for (int k = 0; k < 4 * (R / 32); ++k) {  // 128 channels of 32 rows; thread = channel
-                    const int j = (k % (R / 32)) * 32, ch = k / (R / 32) * 128 + warp * 32 + lane;
-                    const uint32_t at = tmem + lane_base + SH::COL_O + k / (R / 32) * SH::NQ + j;
-                    uint32_t raw[32];
-                    float o[32];
-                    tmem_ld32_nw(at, raw);
+                for (int k = 0; k < 4; ++k) {  // 128 channels of this group's rows; thread = channel
+                    constexpr int N = R / 2;
+                    const int j = wg * N, ch = k * 128 + sub * 32 + lane;
+                    const uint32_t at = tmem + lane_base + SH::COL_O + k * SH::NQ + j;
+                    uint32_t raw[N];
+                    float o[N];
+                    if constexpr (N == 16) tmem_ld16_nw(at, raw);
+                    else tmem_ld32_nw(at, raw);
                     if constexpr (E4M3) {
-                        uint32_t lo[32];
-                        tmem_ld32_nw(at + R, lo);
+                        uint32_t lo[N];
+                        tmem_ld16_nw(at + R, lo);
                         tmem_ld_wait();
                         after_ld_wait(raw);
                         after_ld_wait(lo);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = fmaf(0.0625f, __uint_as_float(lo[i]), __uint_as_float(raw[i]));
+                        for (int i = 0; i < N; ++i) o[i] = fmaf(0.0625f, __uint_as_float(lo[i]), __uint_as_float(raw[i]));
                     } else {
                         tmem_ld_wait();
                         after_ld_wait(raw);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
+                        for (int i = 0; i < N; ++i) o[i] = __uint_as_float(raw[i]);
                     }
                     if (whole) {
                         const float4* f = reinterpret_cast<const float4*>(c.factor + j);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < N / 4; ++i) {
                             const float4 q = f[i];
                             o[4 * i] *= q.x; o[4 * i + 1] *= q.y; o[4 * i + 2] *= q.z; o[4 * i + 3] *= q.w;
                         }
-                        const int have = rows - (row0 + j);  // rows of this sequence among the 32
+                        const int have = rows - (row0 + j);  // rows of this sequence among the N
                         TO* out = static_cast<TO*>(a.o) + (static_cast<int64_t>(seg_w.b) * rows + row0 + j) * kMlaLatent;
                         if constexpr (sizeof(TO) == 2) {
                             // neighbouring lanes swap halves of their rows, so that a lane stores two channels at once:
-                            // an even lane those of rows 0-15, an odd one of rows 16-31
+                            // an even lane those of the first half of the rows, an odd one of the second
                             const bool odd = lane & 1;
-                            out += (odd ? 16 * kMlaLatent : 0) + (ch & ~1);
+                            out += (odd ? N / 2 * kMlaLatent : 0) + (ch & ~1);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 16], 1);
-                                const uint32_t v = odd ? pack_bf16(got, o[i + 16]) : pack_bf16(o[i], got);
-                                if (i + (odd ? 16 : 0) < have) *reinterpret_cast<uint32_t*>(out + i * kMlaLatent) = v;
+                            for (int i = 0; i < N / 2; ++i) {
+                                const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + N / 2], 1);
+                                const uint32_t v = odd ? pack_bf16(got, o[i + N / 2]) : pack_bf16(o[i], got);
+                                if (i + (odd ? N / 2 : 0) < have) *reinterpret_cast<uint32_t*>(out + i * kMlaLatent) = v;
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < N; ++i)
                                 if (i < have) out[i * kMlaLatent + ch] = o[i];
                         }
                     } else {
                         float* out = part.o + (slot * R + j) * kMlaLatent + ch;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) out[i * kMlaLatent] = o[i];
+                        for (int i = 0; i < N; ++i) out[i * kMlaLatent] = o[i];
                     }
                 }
                 tc_fence_before_sync();
-                group_sync(1, 128);  // factor and red are free again
+                group_sync(bar, 128);  // factor and red are free again
                 if (!more) break;
             }
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 9) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
 }
 
 // Joins the partial results of the sequences that the cuts split.  Blocks: (CTA of the main kernel, 128 of the 512
-// channels); the n groups that share a sequence share its rows, n apart.  A warp adds up one row (a lane has 4 channels);
-// where a block has fewer rows than warps, several warps share a row's parts.  Every sum has a fixed order.  The grid is
-// launched while the main kernel runs and waits for its end.
+// channels, which of its two results); the n groups that share a sequence share its rows, n apart.  A warp adds up one
+// row (a lane has 4 channels); of a sequence cut into more than 32 parts the block adds up one row, its warps taking
+// every eighth part.  Every sum has a fixed order.  The time is latency, so loads that do not depend on the
+// weights are issued before them.  The grid is launched while the main kernel runs and waits for its end.
 constexpr int COMBINE = 256;
 
 template <int R, typename TO>
 __global__ void __launch_bounds__(COMBINE) mla_combine_kernel(const __grid_constant__ MlaDecodeArgs a, int row_tiles,
                                                               int ctas) {
+    static_assert(GROUPS <= COMBINE, "a thread per part");
+    constexpr int WARPS = COMBINE / 32, AHEAD = 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int WARPS = COMBINE / 32, MOST = (GROUPS + 31) / 32;
-    __shared__ float wgt[GROUPS > 2 * R ? GROUPS : 2 * R];  // ceil(R / n) n for n <= GROUPS
-    __shared__ float4 acc[WARPS][32];
     const Part p = part_of(a.workspace, ctas, R);
+    const int4 meta = p.meta[blockIdx.x * 2 + blockIdx.z];  // sequence, first and last group
+    if (meta.x < 0) return;
     const int group = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, rows = min(a.S * a.H - rt * R, R);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = blockIdx.y * 128 + lane * 4;
-    for (int which = 0; which < 2; ++which) {
-        const int4 meta = p.meta[blockIdx.x * 2 + which];  // sequence, first and last group
-        if (meta.x < 0) continue;
-        const int n = meta.z - meta.y + 1, first = group - meta.y;
-        const int mine = first < rows ? (rows - first + n - 1) / n : 0;  // rows first, first + n, ...
-        const int64_t base = (static_cast<int64_t>(meta.y) * row_tiles + rt) * 2 * R;
-        auto index = [&](int k, int i) { return base + (static_cast<int64_t>(k) * row_tiles * 2 + (k == 0 ? 1 : 0)) * R + i; };
-        // weights 2^(m_k - m) / l of the block's rows, a warp per row, a lane per part
-        for (int x = warp; x < mine; x += WARPS) {
-            const int i = first + x * n;
-            float f[MOST], m = -INFINITY, l = 0.f;
+    const int n = meta.z - meta.y + 1, first = group - meta.y;
+    const int64_t base = (static_cast<int64_t>(meta.y) * row_tiles + rt) * 2 * R;
+    auto index = [&](int k, int i) { return base + (static_cast<int64_t>(k) * row_tiles * 2 + (k == 0 ? 1 : 0)) * R + i; };
+    auto load = [&](int k, int i) { return __ldcg(reinterpret_cast<const float4*>(p.o + index(k, i) * kMlaLatent + ch)); };
+    auto add = [](float4& o, float f, float4 v) {
+        o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+    };
+    auto store = [&](int i, float4 o, float inv, float m, float l) {
+        const int64_t row = static_cast<int64_t>(meta.x) * a.S * a.H + rt * R + i;
+        TO* out = static_cast<TO*>(a.o) + row * kMlaLatent + ch;
+        if constexpr (sizeof(TO) == 2)
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        else
+            *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (a.lse && blockIdx.y == 0 && lane == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+    };
+    auto warp_max = [](float v) {
 #pragma unroll
-            for (int j = 0; j < MOST; ++j) {
-                const int k = j * 32 + lane;
-                f[j] = k < n ? p.m[index(k, i)] : -INFINITY;
-            }
+        for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    };
+    auto warp_sum = [](float v) {
 #pragma unroll
-            for (int j = 0; j < MOST; ++j) m = fmaxf(m, f[j]);
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    };
+    if (n <= 32) {
+        for (int i = first + warp * n; i < rows; i += WARPS * n) {
+            const float mk = lane < n ? p.m[index(lane, i)] : -INFINITY, lk = lane < n ? p.l[index(lane, i)] : 0.f;
+            float4 v[AHEAD];
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll
-            for (int j = 0; j < MOST; ++j) {
-                const int k = j * 32 + lane;
-                f[j] = f[j] == -INFINITY ? 0.f : ex2(f[j] - m);
-                if (k < n) l = fmaf(f[j], p.l[index(k, i)], l);
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-            for (int j = 0; j < MOST; ++j)
-                if (j * 32 + lane < n) wgt[x * n + j * 32 + lane] = f[j] * inv;
-            if (a.lse && blockIdx.y == 0 && lane == 0)
-                a.lse[static_cast<int64_t>(meta.x) * a.S * a.H + rt * R + i] = (m + log2f(l)) * 0.6931471805599453f;
-        }
-        __syncthreads();
-        const int share = mine >= WARPS ? 1 : mine > 4 ? 1 : mine > 2 ? 2 : mine > 1 ? 4 : 8;  // warps per row
-        const int sub = warp % share;
-        for (int x0 = 0; x0 < mine; x0 += WARPS / share) {
-            const int x = x0 + warp / share, i = first + x * n;
+            for (int k = 0; k < AHEAD; ++k) v[k] = k < n ? load(k, i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float m = warp_max(mk), f = mk == -INFINITY ? 0.f : ex2(mk - m), l = warp_sum(f * lk);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x < mine) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) add(o, __shfl_sync(0xffffffffu, f, k), v[k]);
+#pragma unroll 4
+            for (int k = AHEAD; k < n; ++k) add(o, __shfl_sync(0xffffffffu, f, k), load(k, i));
+            store(i, o, l == 0.f ? 0.f : 1.f / l, m, l);
+        }
+        return;
+    }
+    __shared__ float wgt[GROUPS], red[2][WARPS];
+    __shared__ float4 acc[WARPS][32];
+    for (int i = first; i < rows; i += n) {
+        const int k0 = threadIdx.x;  // this thread's part, for the weights
+        const float mk = k0 < n ? p.m[index(k0, i)] : -INFINITY, lk = k0 < n ? p.l[index(k0, i)] : 0.f;
+        float4 v[AHEAD];  // n > 32 = AHEAD * WARPS
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) v[k] = load(warp + k * WARPS, i);
+        float m = warp_max(mk);
+        if (lane == 0) red[0][warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) m = fmaxf(m, red[0][k]);
+        const float f = mk == -INFINITY ? 0.f : ex2(mk - m);
+        if (k0 < n) wgt[k0] = f;
+        float l = warp_sum(f * lk);
+        if (lane == 0) red[1][warp] = l;
+        __syncthreads();
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) l += red[1][k];
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) add(o, wgt[warp + k * WARPS], v[k]);
 #pragma unroll 8
-                for (int k = sub; k < n; k += share) {
-                    const float g = wgt[x * n + k];
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o + index(k, i) * kMlaLatent + ch));
-                    o.x = fmaf(g, v.x, o.x); o.y = fmaf(g, v.y, o.y); o.z = fmaf(g, v.z, o.z); o.w = fmaf(g, v.w, o.w);
-                }
-            }
-            if (share > 1) {
-                acc[warp][lane] = o;
-                __syncthreads();
-                for (int k = 1; k < share && sub == 0; ++k) {
-                    const float4 v = acc[warp + k][lane];
-                    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-                }
-                __syncthreads();
-            }
-            if (x < mine && sub == 0) {
-                TO* out = static_cast<TO*>(a.o) + (static_cast<int64_t>(meta.x) * a.S * a.H + rt * R + i) * kMlaLatent + ch;
-                if constexpr (sizeof(TO) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-                else *reinterpret_cast<float4*>(out) = o;
-            }
+        for (int k = warp + AHEAD * WARPS; k < n; k += WARPS) add(o, wgt[k], load(k, i));
+        acc[warp][lane] = o;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int k = 1; k < WARPS; ++k) add(o, 1.f, acc[k][lane]);
+            store(i, o, l == 0.f ? 0.f : 1.f / l, m, l);
         }
         __syncthreads();
     }
@@ -921,7 +949,7 @@ cudaError_t launch(const MlaDecodeArgs& a, const Grid& g) {
     err = cudaGetLastError();
     if (err != cudaSuccess || !a.workspace) return err;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, kMlaLatent / 128);
+    cfg.gridDim = dim3(ctas, kMlaLatent / 128, 2);
     cfg.blockDim = dim3(COMBINE);
     cfg.stream = a.stream;
     cudaLaunchAttribute early;

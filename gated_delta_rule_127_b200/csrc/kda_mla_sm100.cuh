@@ -77,6 +77,14 @@ __device__ __forceinline__ void tmem_ld16_x2_nw(uint32_t taddr, uint32_t (&r)[16
         : "r"(taddr), "n"(SPLIT));
 }
 
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld8_x2_nw(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr), "n"(SPLIT));
+}
+
 // One lane of a converged warp.  Products issued under this predicate keep their descriptors in uniform registers:
 // 64 x 32 x 16 products measured 31 cycles apart, against 56 under a lane == 0 test.
 __device__ __forceinline__ bool elect_one() {
@@ -87,19 +95,6 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(p));
     return p != 0u;
-}
-
-// Whether phase `parity` has completed; does not wait.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
 }
 
 // Untiled copy into shared memory (16-byte aligned addresses and size), counted in bytes on `bar`.
@@ -134,10 +129,6 @@ struct RoleWait {
         done = __all_sync(0xffffffffu, done);
         if (!done) give_up();
         return done;
-    }
-    // One look without waiting, for a whole warp.
-    __device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, mbar_test(bar, parity));
     }
 };
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity, 1u << 26); }
