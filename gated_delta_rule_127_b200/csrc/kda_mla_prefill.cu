@@ -15,8 +15,14 @@
 // The reference moves only when a row's maximum exceeds it by 8 in log2 units; then the warp's 32 rows of O and l
 // are multiplied by 2^(old - new).  Until then weights above 1 are as exact as any.
 //
-// Keys and values come through a ring of eight 16 KB pieces (64 channels of 128 keys; 128 channels of 64 values), each
-// with its own barriers: a tile is five pieces, and a piece is free as soon as both sides have used it.
+// Keys and values come through a ring of eight 16 KB pieces (64 channels of 128 keys; 128 channels of 64 values): a tile
+// is three pieces of keys and two of values, and a piece is free as soon as both sides have used it.
+//
+// A thread per side issues its products, in turns: O += W V of a tile and the scores of the next one, then the other
+// thread the same for its side.  Without turns the sides' products mix on the tensor core, both sides' scores come
+// late and together, and the sides fall into step (6,180 cycles a tile); with one thread for both, its looks at barriers
+// (250 cycles each while the softmax warps keep the special-function units' queue full) leave the tensor core idle
+// (4,400 cycles).
 //
 // Roles of the 11 warps: 0-3 and 4-7 the sides' softmax and output, 8 loads (TMA), 9 and 10 issue the sides' products.
 #include <algorithm>
@@ -38,7 +44,7 @@ constexpr int OFF_CTL = OFF_RING + PIECES * PIECE;
 constexpr uint32_t COL_S = 0, COL_O = 256;                // tensor memory: per side 128 columns of each
 
 struct Ctl {
-    uint64_t full[PIECES], empty[PIECES], q_full[2], s_full[2], p_full[2], o_full[2], drain_bar[2];
+    uint64_t k_full[2], v_full[2], empty[PIECES], q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain_bar[2];
     uint32_t tmem, abort_word;
     long long scan[THREADS / 32];
     int b, pair;                       // this CTA's sequence (-1: none) and pair of query tiles
@@ -85,15 +91,16 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (tid == 0) {
             c.abort_word = 0u;
             c.b = -1;
-            for (int i = 0; i < PIECES; ++i) {
-                mbar_init(&c.full[i], 1);
-                mbar_init(&c.empty[i], 2);
-            }
+            for (int i = 0; i < PIECES; ++i) mbar_init(&c.empty[i], 2);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&c.q_full[i], 1);
                 mbar_init(&c.s_full[i], 1);
-                mbar_init(&c.p_full[i], 4);
+                mbar_init(&c.p_full[i][0], 4);
+                mbar_init(&c.p_full[i][1], 4);
                 mbar_init(&c.o_full[i], 1);
+                mbar_init(&c.k_full[i], 1);
+                mbar_init(&c.v_full[i], 1);
+                mbar_init(&c.turn[i], 1);
                 mbar_init(&c.drain_bar[i], 1);
             }
             fence_mbar_init();
@@ -148,6 +155,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             __syncwarp();
             for (int j = 0; j < most && ok; ++j) {
                 const int row = static_cast<int>(k0) + j * ROWS;
+                uint64_t *kb = &c.k_full[j & 1], *vb = &c.v_full[j & 1];
 #pragma unroll
                 for (int k = 0; k < PER_TILE; ++k) {
                     const uint32_t slot = g % PIECES;
@@ -155,22 +163,37 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (!ok) break;
                     if (elect_one()) {
                         unsigned char* dst = smem + OFF_RING + slot * PIECE;
-                        mbar_arrive_expect_tx(&c.full[slot], PIECE);
+                        if (k == 0) mbar_arrive_expect_tx(kb, 3 * PIECE);
+                        if (k == 3) mbar_arrive_expect_tx(vb, 2 * PIECE);
                         if (k < 2) {
-                            tma_load_3d(dst, &tm_k, k * 64, head, row, &c.full[slot]);
+                            tma_load_3d(dst, &tm_k, k * 64, head, row, kb);
                         } else if (k == 2) {
-                            tma_load_3d(dst, &tm_pe, 0, 0, row, &c.full[slot]);
+                            tma_load_3d(dst, &tm_pe, 0, 0, row, kb);
                         } else {
-                            tma_load_3d(dst, &tm_v, kMlaNope, head, row + (k - 3) * 64, &c.full[slot]);
-                            tma_load_3d(dst + PIECE / 2, &tm_v, kMlaNope + 64, head, row + (k - 3) * 64, &c.full[slot]);
+                            tma_load_3d(dst, &tm_v, kMlaNope, head, row + (k - 3) * 64, vb);
+                            tma_load_3d(dst + PIECE / 2, &tm_v, kMlaNope + 64, head, row + (k - 3) * 64, vb);
                         }
                     }
                     __syncwarp();
                     ++g;
                 }
             }
-            if (!ok) {  // let what is in flight land before the block ends
-                for (uint32_t i = g > PIECES ? g - PIECES : 0; i < g; ++i) drain(&c.full[i % PIECES], (i / PIECES) & 1);
+            if (!ok) {
+                // let what is in flight land before the block ends; first what a begun group of pieces still lacks, or its
+                // barrier would never complete
+                const int j = g / PER_TILE, k = g % PER_TILE;
+                if (k != 0 && k != 3 && elect_one()) {
+                    const int row = static_cast<int>(k0) + j * ROWS;
+                    for (int i = k; i < (k < 3 ? 3 : 5); ++i) {
+                        uint64_t* b = k < 3 ? &c.k_full[j & 1] : &c.v_full[j & 1];
+                        unsigned char* dst = smem + OFF_RING + (g - k + i) % PIECES * PIECE;
+                        tma_load_3d(dst, &tm_pe, 0, 0, row, b);  // any piece of this size: nobody reads it
+                    }
+                }
+                __syncwarp();
+                const int last_k = j - (k > 0 ? 0 : 1), last_v = j - (k > 3 ? 0 : 1);  // last tiles begun
+                for (int i = max(last_k - 1, 0); i <= last_k; ++i) drain(&c.k_full[i & 1], (i >> 1) & 1);
+                for (int i = max(last_v - 1, 0); i <= last_v; ++i) drain(&c.v_full[i & 1], (i >> 1) & 1);
                 if (n0 > 0) drain(&c.q_full[0], 0);
                 if (n1 > 0) drain(&c.q_full[1], 0);
             }
@@ -182,57 +205,65 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
             const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
             constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
-            uint32_t g = 0;
-            bool ok = n == 0 || wait(&c.q_full[s], 0);
-            for (int j = 0; j < most && ok; ++j) {
-                if (j >= n) {  // keys that only the other side sees
-                    for (int k = 0; k < PER_TILE && ok; ++k, ++g) {
-                        ok = wait(&c.full[g % PIECES], (g / PIECES) & 1);
-                        if (ok && elect_one()) mbar_arrive(&c.empty[g % PIECES]);
-                        __syncwarp();
-                    }
-                    continue;
-                }
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const uint32_t slot = (g + k) % PIECES;
-                    ok = ok && wait(&c.full[slot], ((g + k) / PIECES) & 1);
-                    if (!ok) break;
+            if (elect_one()) {
+                const auto keys = [&](int j) { return wait.alone(&c.k_full[j & 1], (j >> 1) & 1); };
+                const auto values = [&](int j) { return wait.alone(&c.v_full[j & 1], (j >> 1) & 1); };
+                const auto scores = [&](uint32_t g) {
                     tc_fence_after_sync();
-                    const uint64_t kd = sw128_desc(base + OFF_RING + slot * PIECE, 16, 1024);
-                    if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
-                        mma_commit(&c.empty[slot]);
-                        if (k == 2) mma_commit(&c.s_full[s]);
                     }
-                    __syncwarp();
+                    mma_commit(&c.s_full[s]);
+                };
+                const auto release = [&](uint32_t g, int count) {
+                    for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
+                };
+                bool ok = n == 0 || (wait.alone(&c.q_full[s], 0) && keys(0));
+                if (ok && n > 0) {
+                    scores(0);
+                    release(0, 3);
                 }
-                ok = ok && wait(&c.p_full[s], j & 1);
+                uint32_t g = 0;
+                for (int j = 0; j < n && ok; ++j, g += PER_TILE) {
+                    ok = values(j) && wait.alone(&c.p_full[s][0], j & 1);
+                    if (s == 0) ok = ok && (j == 0 || j > n1 || wait.alone(&c.turn[0], (j - 1) & 1));
+                    else ok = ok && (j >= n0 || wait.alone(&c.turn[1], j & 1));
 #pragma unroll
-                for (int k = 3; k < 5; ++k) {
-                    const uint32_t slot = (g + k) % PIECES;
-                    ok = ok && wait(&c.full[slot], ((g + k) / PIECES) & 1);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint64_t vd = sw128_desc(base + OFF_RING + slot * PIECE, PIECE / 2, 1024);
-                    if (elect_one()) {
+                    for (int k = 0; k < 2; ++k) {
+                        if (k == 1) ok = ok && wait.alone(&c.p_full[s][1], j & 1);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint64_t vd = sw128_desc(base + OFF_RING + (g + 3 + k) % PIECES * PIECE, PIECE / 2, 1024);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)  // 16 keys of 2 x 64 channels
-                            mma_f16_ts(d_o, d_s + (k - 3) * 32 + i * 8, vd + ((i * 2048) >> 4), idesc_o, j > 0 || k + i > 3);
-                        mma_commit(&c.empty[slot]);
-                        if (k == 4 && j + 1 == n) mma_commit(&c.o_full[s]);
+                            mma_f16_ts(d_o, d_s + k * 32 + i * 8, vd + ((i * 2048) >> 4), idesc_o, j > 0 || k + i > 0);
                     }
-                    __syncwarp();
+                    if (ok && j + 1 < n) {
+                        ok = keys(j + 1);
+                        if (ok) scores(g + PER_TILE);
+                    }
+                    if (!ok) break;
+                    mbar_arrive(&c.turn[s ^ 1]);
+                    release(g + 3, 2);
+                    if (j + 1 < n) release(g + PER_TILE, 3);
+                    else mma_commit(&c.o_full[s]);
                 }
-                g += PER_TILE;
+                for (int j = n; j < most && ok; ++j, g += PER_TILE) {  // keys that only the other side sees
+                    ok = keys(j);
+                    for (int k = 0; k < 3 && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
+                    ok = ok && values(j);
+                    for (int k = 3; k < PER_TILE && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
+                }
+                if (!ok) {  // let issued products finish before the block ends
+                    mma_commit(&c.drain_bar[s]);
+                    drain(&c.drain_bar[s], 0);
+                }
             }
-            if (!ok) {  // let issued products finish before the block ends
-                if (elect_one()) mma_commit(&c.drain_bar[s]);
-                __syncwarp();
-                drain(&c.drain_bar[s], 0);
-            }
+            __syncwarp();
         } else {
             // ---------------------------------------------------------------- softmax and output of one side
             const int s = warp >> 2, n = s == 0 ? n0 : n1;
@@ -275,7 +306,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // rows of V past the sequence's end hold whatever lies there: zero them, so that their weight of 0
                     // meets no NaN (both sides do, each before its own product)
                     const uint32_t g = j * PER_TILE + 3;
-                    ok = wait(&c.full[g % PIECES], (g / PIECES) & 1) && wait(&c.full[(g + 1) % PIECES], ((g + 1) / PIECES) & 1);
+                    ok = wait(&c.v_full[j & 1], (j >> 1) & 1);
                     const int r = (warp & 3) * 32 + lane;  // a key of the tile
                     if (ok && r >= nk - j * ROWS) {
                         unsigned char* v = smem + OFF_RING + ((g + (r >> 6)) % PIECES) * PIECE + (r & 63) * 128;
@@ -324,12 +355,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         w[e / 2] = __uint_as_float(pack_bf16(u, v));
                     }
                     tmem_st16(at_s + k * 16, w);
+                    if (k & 1) {  // half of the weights: that half of the second product may begin
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.p_full[s][k >> 1]);
+                    }
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.p_full[s]);
             }
             if (!met) group_sync_or(1 + s, 128, true);
             if (n > 0 && ok) ok = wait(&c.o_full[s], 0);

@@ -118,6 +118,16 @@ struct RoleWait {
         *abort_word = 1u;
         raise_flag(flags, 0x4u);
     }
+    // For one thread: what it waits for is done (the others of its warp learn of a failure from it).
+    __device__ __forceinline__ bool alone(uint64_t* bar, uint32_t parity) const {
+        WaitBudget budget;
+        for (uint32_t i = 0; i < polls; ++i) {
+            if (mbar_poll(bar, parity)) return true;
+            if (((i & 7u) == 7u && aborted()) || budget.expired()) break;
+        }
+        give_up();
+        return false;
+    }
     // Called by whole warps; the answer is the same for all lanes.
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
         WaitBudget budget;
