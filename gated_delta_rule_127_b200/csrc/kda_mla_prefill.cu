@@ -20,11 +20,14 @@
 //
 // A thread per side issues its products, in turns: O += W V of a tile and the scores of the next one, then the other
 // thread the same for its side.  Without turns the sides' products mix on the tensor core, both sides' scores come
-// late and together, and the sides fall into step (6,180 cycles a tile); with one thread for both, its looks at barriers
-// (250 cycles each while the softmax warps keep the special-function units' queue full) leave the tensor core idle
-// (4,400 cycles).
+// late and together, and the sides fall into step (6,180 cycles a tile).  A look at a barrier costs 250 cycles while the
+// softmax warps keep the special-function units' queue full, and the tensor core idles meanwhile; so all that a step
+// waits for (half of its weights, this tile's values, the next one's keys, the other side's turn) arrives at one
+// barrier, `go`, where a warp of its own reports the loads (4,100 cycles with a look at each).
 //
-// Roles of the 11 warps: 0-3 and 4-7 the sides' softmax and output, 8 loads (TMA), 9 and 10 issue the sides' products.
+// Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 loads (TMA), 9 and 10 issue the sides' products, 11
+// reports the loads' arrival.  Registers: 384 threads at 168 when launched, of which the last four warps give up 96 each so that the softmax
+// warps have 216 (a row's 128 scores): 256 x 216 + 128 x 72 = 384 x 168.
 #include <algorithm>
 
 #include "kda_mla_common.cuh"
@@ -37,14 +40,14 @@ namespace {
 using namespace sm100;
 
 constexpr int ROWS = 128;              // queries per side, keys per tile
-constexpr int THREADS = 352;
+constexpr int THREADS = 384;
 constexpr int PIECE = 16384, PIECES = 8, PER_TILE = 5;
 constexpr int OFF_RING = 2 * 3 * PIECE;                   // after both sides' queries (three blocks of 64 channels each)
 constexpr int OFF_CTL = OFF_RING + PIECES * PIECE;
 constexpr uint32_t COL_S = 0, COL_O = 256;                // tensor memory: per side 128 columns of each
 
 struct Ctl {
-    uint64_t k_full[2], v_full[2], empty[PIECES], q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain_bar[2];
+    uint64_t k_full[2], v_full[2], empty[PIECES], q_full[2], s_full[2], go[2], p_full[2], o_full[2], drain_bar[2];
     uint32_t tmem, abort_word;
     long long scan[THREADS / 32];
     int b, pair;                       // this CTA's sequence (-1: none) and pair of query tiles
@@ -95,12 +98,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&c.q_full[i], 1);
                 mbar_init(&c.s_full[i], 1);
-                mbar_init(&c.p_full[i][0], 4);
-                mbar_init(&c.p_full[i][1], 4);
+                mbar_init(&c.go[i], 6);
+                mbar_init(&c.p_full[i], 4);
                 mbar_init(&c.o_full[i], 1);
                 mbar_init(&c.k_full[i], 1);
                 mbar_init(&c.v_full[i], 1);
-                mbar_init(&c.turn[i], 1);
                 mbar_init(&c.drain_bar[i], 1);
             }
             fence_mbar_init();
@@ -137,134 +139,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         const int n0 = tiles(0), n1 = tiles(1), most = max(n0, n1);
 
-        if (warp == 8) {
-            // ---------------------------------------------------------------- loads
-            uint32_t g = 0;
-            bool ok = true;
-            if (most > 0 && elect_one()) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if ((s == 0 ? n0 : n1) == 0) continue;
-                    mbar_arrive_expect_tx(&c.q_full[s], 3 * PIECE);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        tma_load_3d(smem + (s * 3 + k) * PIECE, &tm_q, k * 64, head, static_cast<int>(q0) + i0 + s * ROWS,
-                                    &c.q_full[s]);
-                }
-            }
-            __syncwarp();
-            for (int j = 0; j < most && ok; ++j) {
-                const int row = static_cast<int>(k0) + j * ROWS;
-                uint64_t *kb = &c.k_full[j & 1], *vb = &c.v_full[j & 1];
-#pragma unroll
-                for (int k = 0; k < PER_TILE; ++k) {
-                    const uint32_t slot = g % PIECES;
-                    ok = wait(&c.empty[slot], ((g / PIECES) & 1) ^ 1);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        unsigned char* dst = smem + OFF_RING + slot * PIECE;
-                        if (k == 0) mbar_arrive_expect_tx(kb, 3 * PIECE);
-                        if (k == 3) mbar_arrive_expect_tx(vb, 2 * PIECE);
-                        if (k < 2) {
-                            tma_load_3d(dst, &tm_k, k * 64, head, row, kb);
-                        } else if (k == 2) {
-                            tma_load_3d(dst, &tm_pe, 0, 0, row, kb);
-                        } else {
-                            tma_load_3d(dst, &tm_v, kMlaNope, head, row + (k - 3) * 64, vb);
-                            tma_load_3d(dst + PIECE / 2, &tm_v, kMlaNope + 64, head, row + (k - 3) * 64, vb);
-                        }
-                    }
-                    __syncwarp();
-                    ++g;
-                }
-            }
-            if (!ok) {
-                // let what is in flight land before the block ends; first what a begun group of pieces still lacks, or its
-                // barrier would never complete
-                const int j = g / PER_TILE, k = g % PER_TILE;
-                if (k != 0 && k != 3 && elect_one()) {
-                    const int row = static_cast<int>(k0) + j * ROWS;
-                    for (int i = k; i < (k < 3 ? 3 : 5); ++i) {
-                        uint64_t* b = k < 3 ? &c.k_full[j & 1] : &c.v_full[j & 1];
-                        unsigned char* dst = smem + OFF_RING + (g - k + i) % PIECES * PIECE;
-                        tma_load_3d(dst, &tm_pe, 0, 0, row, b);  // any piece of this size: nobody reads it
-                    }
-                }
-                __syncwarp();
-                const int last_k = j - (k > 0 ? 0 : 1), last_v = j - (k > 3 ? 0 : 1);  // last tiles begun
-                for (int i = max(last_k - 1, 0); i <= last_k; ++i) drain(&c.k_full[i & 1], (i >> 1) & 1);
-                for (int i = max(last_v - 1, 0); i <= last_v; ++i) drain(&c.v_full[i & 1], (i >> 1) & 1);
-                if (n0 > 0) drain(&c.q_full[0], 0);
-                if (n1 > 0) drain(&c.q_full[1], 0);
-            }
-        } else if (warp >= 9) {
-            // ---------------------------------------------------------------- products of one side
-            const int s = warp - 9, n = s == 0 ? n0 : n1;
-            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
-            const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
-            constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
-            if (elect_one()) {
-                const auto keys = [&](int j) { return wait.alone(&c.k_full[j & 1], (j >> 1) & 1); };
-                const auto values = [&](int j) { return wait.alone(&c.v_full[j & 1], (j >> 1) & 1); };
-                const auto scores = [&](uint32_t g) {
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
-                    }
-                    mma_commit(&c.s_full[s]);
-                };
-                const auto release = [&](uint32_t g, int count) {
-                    for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
-                };
-                bool ok = n == 0 || (wait.alone(&c.q_full[s], 0) && keys(0));
-                if (ok && n > 0) {
-                    scores(0);
-                    release(0, 3);
-                }
-                uint32_t g = 0;
-                for (int j = 0; j < n && ok; ++j, g += PER_TILE) {
-                    ok = values(j) && wait.alone(&c.p_full[s][0], j & 1);
-                    if (s == 0) ok = ok && (j == 0 || j > n1 || wait.alone(&c.turn[0], (j - 1) & 1));
-                    else ok = ok && (j >= n0 || wait.alone(&c.turn[1], j & 1));
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (k == 1) ok = ok && wait.alone(&c.p_full[s][1], j & 1);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        const uint64_t vd = sw128_desc(base + OFF_RING + (g + 3 + k) % PIECES * PIECE, PIECE / 2, 1024);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)  // 16 keys of 2 x 64 channels
-                            mma_f16_ts(d_o, d_s + k * 32 + i * 8, vd + ((i * 2048) >> 4), idesc_o, j > 0 || k + i > 0);
-                    }
-                    if (ok && j + 1 < n) {
-                        ok = keys(j + 1);
-                        if (ok) scores(g + PER_TILE);
-                    }
-                    if (!ok) break;
-                    mbar_arrive(&c.turn[s ^ 1]);
-                    release(g + 3, 2);
-                    if (j + 1 < n) release(g + PER_TILE, 3);
-                    else mma_commit(&c.o_full[s]);
-                }
-                for (int j = n; j < most && ok; ++j, g += PER_TILE) {  // keys that only the other side sees
-                    ok = keys(j);
-                    for (int k = 0; k < 3 && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
-                    ok = ok && values(j);
-                    for (int k = 3; k < PER_TILE && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
-                }
-                if (!ok) {  // let issued products finish before the block ends
-                    mma_commit(&c.drain_bar[s]);
-                    drain(&c.drain_bar[s], 0);
-                }
-            }
-            __syncwarp();
-        } else {
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
             // ---------------------------------------------------------------- softmax and output of one side
             const int s = warp >> 2, n = s == 0 ? n0 : n1;
             const int i = i0 + s * ROWS + (warp & 3) * 32 + lane;  // this thread's query
@@ -272,6 +148,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint32_t at_s = tmem + lanes + COL_S + s * 128, at_o = tmem + lanes + COL_O + s * 128;
             // the last key that the query sees, and a scale that is never 0 or negative (scores are negated instead)
             const int see = i < nq ? (a.causal ? min(i + nk - nq, nk - 1) : nk - 1) : -1;
+            const int warp_see = __reduce_min_sync(0xffffffffu, see);  // by the warp's query that sees least
             const float sl2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
             const bool negate = a.scale < 0.f;
             float m = -INFINITY, l = 0.f;
@@ -296,8 +173,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int k = 0; k < ROWS; ++k) x[k] = -x[k];
                 }
-                const int left = see - j * ROWS;  // the last visible column
-                if (__any_sync(0xffffffffu, left < ROWS - 1)) {
+                if (j * ROWS + ROWS - 1 > warp_see) {  // some query of the warp does not see the whole tile
+                    const int left = see - j * ROWS;   // the last column this one sees
 #pragma unroll
                     for (int k = 0; k < ROWS; ++k)
                         if (k > left) x[k] = -INFINITY;
@@ -359,7 +236,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tmem_st_wait();
                         tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&c.p_full[s][k >> 1]);
+                        if (lane == 0) mbar_arrive(k == 1 ? &c.go[s] : &c.p_full[s]);
                     }
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -396,6 +273,148 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
                 if (a.lse && i < nq) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+            }
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            if (warp == 8) {
+                // ---------------------------------------------------------------- loads
+                uint32_t g = 0;
+                bool ok = true;
+                if (most > 0 && elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if ((s == 0 ? n0 : n1) == 0) continue;
+                        mbar_arrive_expect_tx(&c.q_full[s], 3 * PIECE);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            tma_load_3d(smem + (s * 3 + k) * PIECE, &tm_q, k * 64, head, static_cast<int>(q0) + i0 + s * ROWS,
+                                        &c.q_full[s]);
+                    }
+                }
+                __syncwarp();
+                for (int j = 0; j < most && ok; ++j) {
+                    const int row = static_cast<int>(k0) + j * ROWS;
+                    uint64_t *kb = &c.k_full[j & 1], *vb = &c.v_full[j & 1];
+#pragma unroll
+                    for (int k = 0; k < PER_TILE; ++k) {
+                        const uint32_t slot = g % PIECES;
+                        ok = wait(&c.empty[slot], ((g / PIECES) & 1) ^ 1);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            unsigned char* dst = smem + OFF_RING + slot * PIECE;
+                            if (k == 0) mbar_arrive_expect_tx(kb, 3 * PIECE);
+                            if (k == 3) mbar_arrive_expect_tx(vb, 2 * PIECE);
+                            if (k < 2) {
+                                tma_load_3d(dst, &tm_k, k * 64, head, row, kb);
+                            } else if (k == 2) {
+                                tma_load_3d(dst, &tm_pe, 0, 0, row, kb);
+                            } else {
+                                tma_load_3d(dst, &tm_v, kMlaNope, head, row + (k - 3) * 64, vb);
+                                tma_load_3d(dst + PIECE / 2, &tm_v, kMlaNope + 64, head, row + (k - 3) * 64, vb);
+                            }
+                        }
+                        __syncwarp();
+                        ++g;
+                    }
+                }
+                if (!ok) {
+                    // let what is in flight land before the block ends; first what a begun group of pieces still lacks, or its
+                    // barrier would never complete
+                    const int j = g / PER_TILE, k = g % PER_TILE;
+                    if (k != 0 && k != 3 && elect_one()) {
+                        const int row = static_cast<int>(k0) + j * ROWS;
+                        for (int i = k; i < (k < 3 ? 3 : 5); ++i) {
+                            uint64_t* b = k < 3 ? &c.k_full[j & 1] : &c.v_full[j & 1];
+                            unsigned char* dst = smem + OFF_RING + (g - k + i) % PIECES * PIECE;
+                            tma_load_3d(dst, &tm_pe, 0, 0, row, b);  // any piece of this size: nobody reads it
+                        }
+                    }
+                    __syncwarp();
+                    const int last_k = j - (k > 0 ? 0 : 1), last_v = j - (k > 3 ? 0 : 1);  // last tiles begun
+                    for (int i = max(last_k - 1, 0); i <= last_k; ++i) drain(&c.k_full[i & 1], (i >> 1) & 1);
+                    for (int i = max(last_v - 1, 0); i <= last_v; ++i) drain(&c.v_full[i & 1], (i >> 1) & 1);
+                    if (n0 > 0) drain(&c.q_full[0], 0);
+                    if (n1 > 0) drain(&c.q_full[1], 0);
+                }
+            } else if (warp == 9 || warp == 10) {
+                // ---------------------------------------------------------------- products of one side
+                const int s = warp - 9, n = s == 0 ? n0 : n1;
+                const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
+                const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
+                constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
+                if (elect_one()) {
+                    const auto scores = [&](uint32_t g) {
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
+                        }
+                        mma_commit(&c.s_full[s]);
+                    };
+                    const auto release = [&](uint32_t g, int count) {
+                        for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
+                    };
+                    bool ok = n == 0 || (wait.alone(&c.q_full[s], 0) && wait.alone(&c.k_full[0], 0));
+                    if (ok && n > 0) {
+                        scores(0);
+                        release(0, 3);
+                    }
+                    uint32_t g = 0;
+                    for (int j = 0; j < n && ok; ++j, g += PER_TILE) {
+                        if (s == 0 ? j == 0 || j > n1 : j >= n0) mbar_arrive(&c.go[s]);  // no other side to wait for
+                        ok = wait.alone(&c.go[s], j & 1);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (k == 1) ok = ok && wait.alone(&c.p_full[s], j & 1);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            const uint64_t vd = sw128_desc(base + OFF_RING + (g + 3 + k) % PIECES * PIECE, PIECE / 2, 1024);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)  // 16 keys of 2 x 64 channels
+                                mma_f16_ts(d_o, d_s + k * 32 + i * 8, vd + ((i * 2048) >> 4), idesc_o, j > 0 || k + i > 0);
+                            release(g + 3 + k, 1);  // before the scores: what a commit reports is all that came before it
+                        }
+                        if (ok && j + 1 < n) {
+                            ok = wait.alone(&c.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+                            if (ok) scores(g + PER_TILE);
+                        }
+                        if (!ok) break;
+                        if (s == 0 ? j < n1 : j + 1 < n0) mbar_arrive(&c.go[s ^ 1]);  // the other side's turn
+                        if (j + 1 < n) release(g + PER_TILE, 3);
+                        else mma_commit(&c.o_full[s]);
+                    }
+                    for (int j = n; j < most && ok; ++j, g += PER_TILE) {  // keys that only the other side sees
+                        ok = wait.alone(&c.k_full[j & 1], (j >> 1) & 1);
+                        for (int k = 0; k < 3 && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
+                        ok = ok && wait.alone(&c.v_full[j & 1], (j >> 1) & 1);
+                        for (int k = 3; k < PER_TILE && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
+                    }
+                    if (!ok) {  // let issued products finish before the block ends
+                        mma_commit(&c.drain_bar[s]);
+                        drain(&c.drain_bar[s], 0);
+                    }
+                }
+                __syncwarp();
+            } else {
+                // ---------------------------------------------------------------- arrivals: tells the sides' steps of them
+                if (elect_one()) {
+                    bool ok = true;
+                    for (int j = 0; j < most && ok; ++j) {
+                        ok = wait.alone(&c.v_full[j & 1], (j >> 1) & 1);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (j >= (s == 0 ? n0 : n1)) continue;
+                            ok = ok && (j == 0 || wait.alone(&c.go[s], (j - 1) & 1));  // one step at a time
+                            if (ok) mbar_arrive(&c.go[s]);
+                        }
+                    }
+                }
+                __syncwarp();
             }
         }
     }
