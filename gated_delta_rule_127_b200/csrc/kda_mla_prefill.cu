@@ -21,9 +21,9 @@
 // A thread per side issues its products, in turns: O += W V of a tile and the scores of the next one, then the other
 // thread the same for its side.  Without turns the sides' products mix on the tensor core, both sides' scores come
 // late and together, and the sides fall into step (6,180 cycles a tile).  A look at a barrier costs 250 cycles while the
-// softmax warps keep the special-function units' queue full, and the tensor core idles meanwhile; so all that a step
-// waits for (half of its weights, this tile's values, the next one's keys, the other side's turn) arrives at one
-// barrier, `go`, where a warp of its own reports the loads (4,100 cycles with a look at each).
+// softmax warps keep the special-function units' queue full, and the tensor core idles meanwhile; so a step looks at two:
+// `go` for half of its weights, this tile's values and the other side's turn, `p_full` for the other half and the next
+// tile's keys.  A warp of its own reports the loads there (4,100 cycles with a look at each barrier).
 //
 // Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 loads (TMA), 9 and 10 issue the sides' products, 11
 // reports the loads' arrival.  Registers: 384 threads at 168 when launched, of which the last four warps give up 96 each so that the softmax
@@ -99,7 +99,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 mbar_init(&c.q_full[i], 1);
                 mbar_init(&c.s_full[i], 1);
                 mbar_init(&c.go[i], 6);
-                mbar_init(&c.p_full[i], 4);
+                mbar_init(&c.p_full[i], 5);
                 mbar_init(&c.o_full[i], 1);
                 mbar_init(&c.k_full[i], 1);
                 mbar_init(&c.v_full[i], 1);
@@ -173,7 +173,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int k = 0; k < ROWS; ++k) x[k] = -x[k];
                 }
-                if (j * ROWS + ROWS - 1 > warp_see) {  // some query of the warp does not see the whole tile
+                const bool edge = j * ROWS + ROWS - 1 > warp_see;  // some query of the warp does not see the whole tile
+                if (edge) {
                     const int left = see - j * ROWS;   // the last column this one sees
 #pragma unroll
                     for (int k = 0; k < ROWS; ++k)
@@ -223,21 +224,22 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float w[16];
+                    uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float u = ex2(fmaf(x[k * 32 + e], sl2, -ref)), v = ex2(fmaf(x[k * 32 + e + 1], sl2, -ref));
                         sum[e & 2] += u;
                         sum[(e & 2) + 1] += v;
-                        w[e / 2] = __uint_as_float(pack_bf16(u, v));
+                        w[e / 2] = pack_bf16(u, v);
                     }
-                    tmem_st16(at_s + k * 16, w);
-                    if (k & 1) {  // half of the weights: that half of the second product may begin
+                    if (k == 3) tmem_st16_nw(at_s + k * 16, w);
+                    if (k >= 2) {  // the first half is announced when the third quarter has been computed: its stores have landed
                         tmem_st_wait();
                         tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(k == 1 ? &c.go[s] : &c.p_full[s]);
+                        if (lane == 0) mbar_arrive(k == 2 ? &c.go[s] : &c.p_full[s]);
                     }
+                    if (k < 3) tmem_st16_nw(at_s + k * 16, w);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
@@ -379,11 +381,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 mma_f16_ts(d_o, d_s + k * 32 + i * 8, vd + ((i * 2048) >> 4), idesc_o, j > 0 || k + i > 0);
                             release(g + 3 + k, 1);  // before the scores: what a commit reports is all that came before it
                         }
-                        if (ok && j + 1 < n) {
-                            ok = wait.alone(&c.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
-                            if (ok) scores(g + PER_TILE);
-                        }
                         if (!ok) break;
+                        if (j + 1 < n) scores(g + PER_TILE);
                         if (s == 0 ? j < n1 : j + 1 < n0) mbar_arrive(&c.go[s ^ 1]);  // the other side's turn
                         if (j + 1 < n) release(g + PER_TILE, 3);
                         else mma_commit(&c.o_full[s]);
@@ -407,10 +406,17 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int j = 0; j < most && ok; ++j) {
                         ok = wait.alone(&c.v_full[j & 1], (j >> 1) & 1);
 #pragma unroll
+                        for (int s = 0; s < 2; ++s) {  // one step at a time, here and below
+                            if (j >= (s == 0 ? n0 : n1)) continue;
+                            ok = ok && (j == 0 || wait.alone(&c.go[s], (j - 1) & 1));
+                            if (ok) mbar_arrive(&c.go[s]);
+                        }
+                        if (j + 1 < most) ok = ok && wait.alone(&c.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+#pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             if (j >= (s == 0 ? n0 : n1)) continue;
-                            ok = ok && (j == 0 || wait.alone(&c.go[s], (j - 1) & 1));  // one step at a time
-                            if (ok) mbar_arrive(&c.go[s]);
+                            ok = ok && (j == 0 || wait.alone(&c.p_full[s], (j - 1) & 1));
+                            if (ok) mbar_arrive(&c.p_full[s]);
                         }
                     }
                 }

@@ -66,6 +66,15 @@ __device__ __forceinline__ uint32_t sw64_byte(int row, int col) {
     return static_cast<uint32_t>(row * 64 + ((((col >> 4) ^ (row >> 1)) & 3) << 4) + (col & 15));
 }
 
+// Registers -> tensor memory: 32 lanes x 16 consecutive 32-bit columns per warp.
+__device__ __forceinline__ void tmem_st16_nw(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+
 // 16 lanes read twice, as tmem_ld16_x2, without waiting.
 template <int SPLIT>
 __device__ __forceinline__ void tmem_ld16_x2_nw(uint32_t taddr, uint32_t (&r)[16]) {
