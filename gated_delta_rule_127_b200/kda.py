@@ -6,6 +6,7 @@ every step of the computation runs in libkda's CUDA kernels.  There is no fallba
 missing or was built without the kernels, the first call raises.
 """
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -365,51 +366,79 @@ def _decode(entry, q, k, v, log_alpha, beta, state, o, dtype_o, stream, options=
 
 # ---- latent attention
 
-def _mla_cache_dtype(t: torch.Tensor) -> int:
-    if t.dtype == torch.float8_e4m3fn:
-        return KDA_E4M3
-    if t.dtype == torch.bfloat16:
-        return KDA_BF16
-    raise TypeError(f"cache_latent must be bfloat16 or float8_e4m3fn, got {t.dtype}")
+
+def _on_stream(fn):
+    """Runs fn with the device of its first tensor and, where the caller names one, its stream current: what fn
+    allocates then belongs to the stream that uses it, so that no freed buffer is handed out too early."""
+    name = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw[name]
+        index = first.get_device()
+        if index < 0 or (stream is None and index == torch.cuda.current_device()):
+            return fn(*args, **kw)
+        with torch.cuda.device(index):
+            if stream is None:
+                return fn(*args, **kw)
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream_handle(stream), first.device)
+            if stream.device != first.device:
+                raise ValueError(f"the stream belongs to {stream.device}, the tensors to {first.device}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
+    return call
 
 
-def _mla_index(t: torch.Tensor, what: str, shape) -> None:
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+def _mla_check(device, **tensors) -> None:
+    index = device.index
+    for t in tensors.values():
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            _check_cuda(tensors, device)
+
+
+def _mla_index(t: torch.Tensor, what: str, n: int) -> None:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what} must be int32 [{n}], got {t.dtype} {list(t.shape)}")
 
 
 def _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table):
-    """Checks the paged cache's tensors; returns (dtype code, num_pages, page_size, B, max_pages)."""
-    code = _mla_cache_dtype(cache_latent)
+    """Checks the paged cache's tensors; returns (dtype code, num_pages, page_size, d_latent, d_pe, B, max_pages)."""
+    if cache_latent.dtype == torch.float8_e4m3fn:
+        code = KDA_E4M3
+    elif cache_latent.dtype == torch.bfloat16:
+        code = KDA_BF16
+    else:
+        raise TypeError(f"cache_latent must be bfloat16 or float8_e4m3fn, got {cache_latent.dtype}")
     if cache_latent.dim() != 3 or cache_pe.dim() != 3 or cache_latent.shape[:2] != cache_pe.shape[:2]:
         raise ValueError("expected cache_latent [num_pages, page_size, d_latent], cache_pe [num_pages, page_size, d_pe]")
     if cache_pe.dtype != torch.bfloat16:
         raise TypeError(f"cache_pe must be bfloat16, got {cache_pe.dtype}")
+    pages, page, dl = cache_latent.shape
     if (cache_scale is None) == (code == KDA_E4M3):
         raise ValueError("cache_scale goes with a float8_e4m3fn cache, and only with one")
-    if cache_scale is not None and (cache_scale.dtype != torch.float32 or cache_scale.shape != cache_latent.shape[:2]):
+    if cache_scale is not None and (cache_scale.dtype != torch.float32 or cache_scale.shape != (pages, page)):
         raise ValueError("cache_scale must be fp32 [num_pages, page_size]")
     if page_table.dtype != torch.int32 or page_table.dim() != 2:
         raise ValueError("page_table must be int32 [B, max_pages]")
-    return code, cache_latent.shape[0], cache_latent.shape[1], page_table.shape[0], page_table.shape[1]
+    B, width = page_table.shape
+    return code, pages, page, dl, cache_pe.shape[2], B, width
 
 
-def _mla_call(device, stream, ts, new, call):
-    """Checks the tensors `ts`, allocates with new() on the stream of the call (so that a freed buffer is not
-    handed out again before the stream is past it) and launches with call(allocated, stream handle)."""
-    _check_cuda(ts, device)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _mla_call(device, stream, {}, new, call)
-    if stream is None:
-        got = new()
-        return got, call(got, torch.cuda.current_stream().cuda_stream)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream), device)
-    with torch.cuda.stream(s):
-        got = new()
-    return got, call(got, _stream_handle(stream))
+def _mla_out(given, what, like, shape, dtype):
+    """The given output tensor, checked, or a new one on the device of `like`."""
+    if given is None:
+        return like.new_empty(shape, dtype=dtype)
+    if given.shape != shape or given.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+    return given
 
 
+def _mla_raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@_on_stream
 def kda_mla_cache_write(latent: torch.Tensor, pe: torch.Tensor, cache_latent: torch.Tensor, cache_pe: torch.Tensor,
                         page_table: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *,
                         cache_scale: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -420,28 +449,27 @@ def kda_mla_cache_write(latent: torch.Tensor, pe: torch.Tensor, cache_latent: to
     [B, max_pages] int32; seq_lens [B] int32, the new tokens included; cu_seqlens [B+1] int32 or None (the same
     number of new tokens for each sequence).  The cache tensors are updated in place.
     """
-    lib = load_library()
-    code, pages, page, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
-    if latent.dim() != 2 or pe.dim() != 2 or latent.shape[0] != pe.shape[0] or \
-            latent.shape[1] != cache_latent.shape[2] or pe.shape[1] != cache_pe.shape[2]:
+    code, pages, page, dl, dp, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
+    T = latent.shape[0]
+    if latent.shape != (T, dl) or pe.shape != (T, dp):
         raise ValueError("expected latent [T, d_latent] and pe [T, d_pe] with the cache's channels")
     if latent.dtype != pe.dtype:
         raise TypeError("latent and pe must share a dtype")
-    dt = _dtype_code(latent, "latent")
-    _mla_index(seq_lens, "seq_lens", (B,))
+    _mla_index(seq_lens, "seq_lens", B)
     if cu_seqlens is not None:
-        _mla_index(cu_seqlens, "cu_seqlens", (B + 1,))
-    _, st = _mla_call(
-        latent.device, stream,
-        dict(latent=latent, pe=pe, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale,
-             page_table=page_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens), lambda: None,
-        lambda _, handle: lib.kda_mla_cache_write(
-            _ptr(latent), _ptr(pe), _ptr(cu_seqlens), _ptr(seq_lens), latent.shape[0], B, latent.shape[1], pe.shape[1],
-            dt, code, _ptr(cache_latent), _ptr(cache_pe), _ptr(cache_scale), _ptr(page_table), pages, page, width, handle))
+        _mla_index(cu_seqlens, "cu_seqlens", B + 1)
+    device = latent.device
+    _mla_check(device, latent=latent, pe=pe, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale,
+               page_table=page_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens)
+    st = load_library().kda_mla_cache_write(
+        latent.data_ptr(), pe.data_ptr(), _ptr(cu_seqlens), seq_lens.data_ptr(), T, B, dl, dp, _dtype_code(latent, "latent"),
+        code, cache_latent.data_ptr(), cache_pe.data_ptr(), _ptr(cache_scale), page_table.data_ptr(), pages, page, width,
+        _mla_raw_stream(device))
     if st != KDA_OK:
         raise KdaError(st, "kda_mla_cache_write")
 
 
+@_on_stream
 def kda_mla_cache_read(cache_latent: torch.Tensor, cache_pe: torch.Tensor, page_table: torch.Tensor,
                        cu_seqlens: Optional[torch.Tensor], T: int, *, starts: Optional[torch.Tensor] = None,
                        cache_scale: Optional[torch.Tensor] = None, latent: Optional[torch.Tensor] = None,
@@ -454,42 +482,34 @@ def kda_mla_cache_read(cache_latent: torch.Tensor, cache_pe: torch.Tensor, page_
     (latent [T, 512], pe [T, 64]) in dtype_o (bf16 by default), the given tensors where there are any; rows
     that nothing is read into are left as they were (undefined in arrays allocated here).
     """
-    lib = load_library()
-    code, pages, page, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
+    code, pages, page, dl, dp, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
     if cu_seqlens is not None:
-        _mla_index(cu_seqlens, "cu_seqlens", (B + 1,))
+        _mla_index(cu_seqlens, "cu_seqlens", B + 1)
     if starts is not None:
-        _mla_index(starts, "starts", (B,))
-    T, dl, dp = int(T), cache_latent.shape[2], cache_pe.shape[2]
+        _mla_index(starts, "starts", B)
     if T < 0:
         raise ValueError("T must not be negative")
     if dtype_o is None:
         dtype_o = latent.dtype if latent is not None else pe.dtype if pe is not None else torch.bfloat16
-    for t, what, d in ((latent, "latent", dl), (pe, "pe", dp)):
-        if t is not None and (tuple(t.shape) != (T, d) or t.dtype != dtype_o):
-            raise ValueError(f"{what} must be {dtype_o} [{T}, {d}]")
     device = cache_latent.device
-
-    def new():
-        return (torch.empty((T, dl), dtype=dtype_o, device=device) if latent is None else latent,
-                torch.empty((T, dp), dtype=dtype_o, device=device) if pe is None else pe)
-
-    got, st = _mla_call(
-        device, stream,
-        dict(cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale, page_table=page_table,
-             cu_seqlens=cu_seqlens, starts=starts, latent=latent, pe=pe), new,
-        lambda got, handle: lib.kda_mla_cache_read(
-            _ptr(cache_latent), _ptr(cache_pe), _ptr(cache_scale), _ptr(page_table), _ptr(cu_seqlens), _ptr(starts), T, B,
-            dl, dp, pages, page, width, code, _dtype_code(got[0], "dtype_o"), _ptr(got[0]), _ptr(got[1]), handle))
+    _mla_check(device, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale, page_table=page_table,
+               cu_seqlens=cu_seqlens, starts=starts, latent=latent, pe=pe)
+    latent = _mla_out(latent, "latent", cache_pe, (T, dl), dtype_o)
+    pe = _mla_out(pe, "pe", cache_pe, (T, dp), dtype_o)
+    st = load_library().kda_mla_cache_read(
+        cache_latent.data_ptr(), cache_pe.data_ptr(), _ptr(cache_scale), page_table.data_ptr(), _ptr(cu_seqlens),
+        _ptr(starts), T, B, dl, dp, pages, page, width, code, _dtype_code(latent, "dtype_o"), latent.data_ptr(),
+        pe.data_ptr(), _mla_raw_stream(device))
     if st != KDA_OK:
         raise KdaError(st, "kda_mla_cache_read")
-    return got
+    return latent, pe
 
 
 def kda_mla_decode_workspace_size(B: int, S: int, H: int, d_latent: int = 512, d_pe: int = 64) -> int:
     return int(load_library().kda_mla_decode_workspace_size(B, S, H, d_latent, d_pe))
 
 
+@_on_stream
 def kda_mla_decode(q_latent: torch.Tensor, q_pe: torch.Tensor, cache_latent: torch.Tensor, cache_pe: torch.Tensor,
                    page_table: torch.Tensor, seq_lens: torch.Tensor, *, softmax_scale: float,
                    cache_scale: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
@@ -500,53 +520,40 @@ def kda_mla_decode(q_latent: torch.Tensor, q_pe: torch.Tensor, cache_latent: tor
 
     q_latent [B, S, H, 512], q_pe [B, S, H, 64] bf16; the cache as in kda_mla_cache_write; seq_lens [B] int32, the
     new tokens included.  Returns (o [B, S, H, 512] in dtype_o, lse [B, S, H] fp32 or None).  A workspace of
-    kda_mla_decode_workspace_size bytes is allocated when none is given; with use_workspace=False none is
-    passed and no sequence is split over several SMs.
+    kda_mla_decode_workspace_size bytes is allocated when none is given (or one that is too small); with
+    use_workspace=False none is passed and no sequence is split over several SMs.
     """
     lib = load_library()
-    code, pages, page, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
-    if q_latent.dim() != 4 or q_pe.dim() != 4 or q_latent.shape[:3] != q_pe.shape[:3] or q_latent.shape[0] != B or \
-            q_latent.shape[3] != cache_latent.shape[2] or q_pe.shape[3] != cache_pe.shape[2]:
+    code, pages, page, dl, dp, B, width = _mla_cache_args(cache_latent, cache_pe, cache_scale, page_table)
+    shape = q_latent.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != dl or q_pe.shape != (B, shape[1], shape[2], dp):
         raise ValueError("expected q_latent [B, S, H, d_latent] and q_pe [B, S, H, d_pe] with the cache's channels")
-    _, S, H, dl = q_latent.shape
-    dp = q_pe.shape[3]
+    _, S, H, _ = shape
     if q_latent.dtype != q_pe.dtype:
         raise TypeError("q_latent and q_pe must share a dtype")
-    dq = _dtype_code(q_latent, "q_latent")
-    _mla_index(seq_lens, "seq_lens", (B,))
-    if dtype_o is None:
-        dtype_o = o.dtype if o is not None else q_latent.dtype
-    if o is not None and (tuple(o.shape) != (B, S, H, dl) or o.dtype != dtype_o):
-        raise ValueError(f"o must be {dtype_o} {[B, S, H, dl]}")
-    if lse is not None and (tuple(lse.shape) != (B, S, H) or lse.dtype != torch.float32):
-        raise ValueError(f"lse must be fp32 {[B, S, H]}")
+    _mla_index(seq_lens, "seq_lens", B)
     device = q_latent.device
+    _mla_check(device, q_latent=q_latent, q_pe=q_pe, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale,
+               page_table=page_table, seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
+    o = _mla_out(o, "o", q_latent, shape, dtype_o or (q_latent.dtype if o is None else o.dtype))
+    if lse is not None or output_lse:
+        lse = _mla_out(lse, "lse", q_latent, shape[:3], torch.float32)
     need = lib.kda_mla_decode_workspace_size(B, S, H, dl, dp) if use_workspace else 0
-
-    def new():
-        ws = None
-        if need > 0:
-            ws = workspace
-            if ws is None or ws.numel() * ws.element_size() < need:
-                ws = torch.empty(need, dtype=torch.uint8, device=device)
-        return (torch.empty((B, S, H, dl), dtype=dtype_o, device=device) if o is None else o,
-                torch.empty((B, S, H), dtype=torch.float32, device=device) if lse is None and output_lse else lse, ws)
-
-    def call(got, handle):
-        ws = got[2]
-        return lib.kda_mla_decode(
-            _ptr(q_latent), _ptr(q_pe), _ptr(cache_latent), _ptr(cache_pe), _ptr(cache_scale), _ptr(page_table),
-            _ptr(seq_lens), B, S, H, dl, dp, pages, page, width, softmax_scale, dq, code, _dtype_code(got[0], "o"),
-            _ptr(got[0]), _ptr(got[1]), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), handle)
-
-    got, st = _mla_call(device, stream, dict(q_latent=q_latent, q_pe=q_pe, cache_latent=cache_latent, cache_pe=cache_pe,
-                                             cache_scale=cache_scale, page_table=page_table, seq_lens=seq_lens, o=o,
-                                             lse=lse, workspace=workspace), new, call)
+    if need == 0:
+        workspace = None
+    elif workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = q_latent.new_empty(need, dtype=torch.uint8)
+    st = lib.kda_mla_decode(
+        q_latent.data_ptr(), q_pe.data_ptr(), cache_latent.data_ptr(), cache_pe.data_ptr(), _ptr(cache_scale),
+        page_table.data_ptr(), seq_lens.data_ptr(), B, S, H, dl, dp, pages, page, width, softmax_scale,
+        _dtype_code(q_latent, "q_latent"), code, _dtype_code(o, "o"), o.data_ptr(), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _mla_raw_stream(device))
     if st != KDA_OK:
         raise KdaError(st, "kda_mla_decode")
-    return got[0], got[1]
+    return o, lse
 
 
+@_on_stream
 def kda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor] = None,
                     cu_seqlens_k: Optional[torch.Tensor] = None, *, softmax_scale: float, num_seqs: Optional[int] = None,
                     causal: bool = True, o: Optional[torch.Tensor] = None, dtype_o: Optional[torch.dtype] = None,
@@ -558,7 +565,6 @@ def kda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_se
     one or none; without them `num_seqs` sequences of equal lengths, default 1).  Returns
     (o [Tq, H, 128] in dtype_o, lse [Tq, H] fp32 or None).  Rows behind the last sequence are not written.
     """
-    lib = load_library()
     if q.dim() != 3 or kv.dim() != 3 or k_pe.dim() != 2 or kv.shape[1] != q.shape[1] or k_pe.shape[0] != kv.shape[0]:
         raise ValueError("expected q [Tq, H, d_nope + d_pe], kv [Tk, H, d_nope + dv], k_pe [Tk, d_pe]")
     Tq, H, dqk = q.shape
@@ -568,32 +574,23 @@ def kda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_se
         raise ValueError("the channels of q, kv and k_pe do not fit together")
     if q.dtype != kv.dtype or q.dtype != k_pe.dtype:
         raise TypeError("q, kv, k_pe must share a dtype")
-    dt = _dtype_code(q, "q")
-    given = [c for c in (cu_seqlens_q, cu_seqlens_k) if c is not None]
-    B = given[0].numel() - 1 if given else 1 if num_seqs is None else int(num_seqs)
+    given = cu_seqlens_q if cu_seqlens_q is not None else cu_seqlens_k
+    B = given.numel() - 1 if given is not None else 1 if num_seqs is None else int(num_seqs)
     for c, what in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k")):
         if c is not None:
-            _mla_index(c, what, (B + 1,))
-    if dtype_o is None:
-        dtype_o = o.dtype if o is not None else q.dtype
-    if o is not None and (tuple(o.shape) != (Tq, H, dv) or o.dtype != dtype_o):
-        raise ValueError(f"o must be {dtype_o} {[Tq, H, dv]}")
-    if lse is not None and (tuple(lse.shape) != (Tq, H) or lse.dtype != torch.float32):
-        raise ValueError(f"lse must be fp32 {[Tq, H]}")
+            _mla_index(c, what, B + 1)
     device = q.device
-
-    def new():
-        return (torch.empty((Tq, H, dv), dtype=dtype_o, device=device) if o is None else o,
-                torch.empty((Tq, H), dtype=torch.float32, device=device) if lse is None and output_lse else lse)
-
-    got, st = _mla_call(
-        device, stream, dict(q=q, kv=kv, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, o=o, lse=lse),
-        new, lambda got, handle: lib.kda_mla_prefill(
-            _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), Tq, Tk, B, H, dn, dp, dv,
-            1 if causal else 0, softmax_scale, dt, _dtype_code(got[0], "o"), _ptr(got[0]), _ptr(got[1]), handle))
+    _mla_check(device, q=q, kv=kv, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, o=o, lse=lse)
+    o = _mla_out(o, "o", q, (Tq, H, dv), dtype_o or (q.dtype if o is None else o.dtype))
+    if lse is not None or output_lse:
+        lse = _mla_out(lse, "lse", q, (Tq, H), torch.float32)
+    st = load_library().kda_mla_prefill(
+        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), Tq, Tk, B, H, dn, dp, dv,
+        1 if causal else 0, softmax_scale, _dtype_code(q, "q"), _dtype_code(o, "o"), o.data_ptr(), _ptr(lse),
+        _mla_raw_stream(device))
     if st != KDA_OK:
         raise KdaError(st, "kda_mla_prefill")
-    return got
+    return o, lse
 
 
 def kda_get_device_status(stream=None) -> Tuple[int, int]:
