@@ -492,10 +492,10 @@ def kda_mla_cache_read(cache_latent: torch.Tensor, cache_pe: torch.Tensor, page_
     if dtype_o is None:
         dtype_o = latent.dtype if latent is not None else pe.dtype if pe is not None else torch.bfloat16
     device = cache_latent.device
-    _mla_check(device, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale, page_table=page_table,
-               cu_seqlens=cu_seqlens, starts=starts, latent=latent, pe=pe)
     latent = _mla_out(latent, "latent", cache_pe, (T, dl), dtype_o)
     pe = _mla_out(pe, "pe", cache_pe, (T, dp), dtype_o)
+    _mla_check(device, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale, page_table=page_table,
+               cu_seqlens=cu_seqlens, starts=starts, latent=latent, pe=pe)
     st = load_library().kda_mla_cache_read(
         cache_latent.data_ptr(), cache_pe.data_ptr(), _ptr(cache_scale), page_table.data_ptr(), _ptr(cu_seqlens),
         _ptr(starts), T, B, dl, dp, pages, page, width, code, _dtype_code(latent, "dtype_o"), latent.data_ptr(),
@@ -533,11 +533,11 @@ def kda_mla_decode(q_latent: torch.Tensor, q_pe: torch.Tensor, cache_latent: tor
         raise TypeError("q_latent and q_pe must share a dtype")
     _mla_index(seq_lens, "seq_lens", B)
     device = q_latent.device
-    _mla_check(device, q_latent=q_latent, q_pe=q_pe, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale,
-               page_table=page_table, seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
     o = _mla_out(o, "o", q_latent, shape, dtype_o or (q_latent.dtype if o is None else o.dtype))
     if lse is not None or output_lse:
         lse = _mla_out(lse, "lse", q_latent, shape[:3], torch.float32)
+    _mla_check(device, q_latent=q_latent, q_pe=q_pe, cache_latent=cache_latent, cache_pe=cache_pe, cache_scale=cache_scale,
+               page_table=page_table, seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
     need = lib.kda_mla_decode_workspace_size(B, S, H, dl, dp) if use_workspace else 0
     if need == 0:
         workspace = None
@@ -580,10 +580,10 @@ def kda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_se
         if c is not None:
             _mla_index(c, what, B + 1)
     device = q.device
-    _mla_check(device, q=q, kv=kv, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, o=o, lse=lse)
     o = _mla_out(o, "o", q, (Tq, H, dv), dtype_o or (q.dtype if o is None else o.dtype))
     if lse is not None or output_lse:
         lse = _mla_out(lse, "lse", q, (Tq, H), torch.float32)
+    _mla_check(device, q=q, kv=kv, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, o=o, lse=lse)
     st = load_library().kda_mla_prefill(
         q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), Tq, Tk, B, H, dn, dp, dv,
         1 if causal else 0, softmax_scale, _dtype_code(q, "q"), _dtype_code(o, "o"), o.data_ptr(), _ptr(lse),
