@@ -293,7 +293,7 @@ const char* kda_status_string(kda_status status) {
     return "unknown status";
 }
 
-uint32_t kda_version(void) { return (1u << 16) | 0u; }
+uint32_t kda_version(void) { return (1u << 16) | 1u; }
 
 void kda_testing_set_wait_limit(int64_t polls) {
     const uint32_t v = polls < 0 ? kda::kDefaultWaitPolls

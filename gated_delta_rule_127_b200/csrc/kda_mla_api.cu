@@ -14,6 +14,9 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool plain_dtype(kda_dtype d) { return d == KDA_BF16 || d == KDA_FP32; }
 bool given16(const void* p) { return p && aligned16(p); }
 
+// Rows and positions are 32-bit numbers in the kernels, also those just past a last tile of 256.
+constexpr int64_t kMostRows = 0x7fffff00;
+
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
     ~NvtxRange() { nvtxRangePop(); }
@@ -28,7 +31,7 @@ kda_status check_cache(const void* latent, const void* pe, const float* scale, c
         return dtype_cache == KDA_FP32 ? KDA_ERR_UNSUPPORTED : KDA_ERR_INVALID_ARG;
     if (d_latent != kMlaLatent || d_pe != kMlaPe) return KDA_ERR_UNSUPPORTED;
     if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return KDA_ERR_UNSUPPORTED;
-    if (num_pages * page_size > 0x7fffffffLL || static_cast<int64_t>(max_pages) * page_size > 0x7fffffffLL)
+    if (num_pages > kMostRows / page_size || static_cast<int64_t>(max_pages) * page_size > kMostRows)
         return KDA_ERR_UNSUPPORTED;
     const bool e4m3 = dtype_cache == KDA_E4M3;
     if (used) {
@@ -87,7 +90,7 @@ kda_status kda_mla_cache_write(const void* latent, const void* pe, const int32_t
     const kda_status st = check_cache(cache_latent, cache_pe, cache_scale, page_table, d_latent, d_pe, num_pages,
                                       page_size, max_pages, dtype_cache, T > 0, &c);
     if (st != KDA_OK) return st;
-    if (T > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (T > kMostRows) return KDA_ERR_UNSUPPORTED;
     if (!cu_seqlens && T % B != 0) return KDA_ERR_INVALID_ARG;
     return cache_copy(true, latent, pe, cu_seqlens, seq_lens, T, B, dtype_in, c, stream);
 }
@@ -102,7 +105,7 @@ kda_status kda_mla_cache_read(const void* cache_latent, const void* cache_pe, co
     const kda_status st = check_cache(cache_latent, cache_pe, cache_scale, page_table, d_latent, d_pe, num_pages,
                                       page_size, max_pages, dtype_cache, T > 0, &c);
     if (st != KDA_OK) return st;
-    if (T > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (T > kMostRows) return KDA_ERR_UNSUPPORTED;
     if (!cu_seqlens && T % B != 0) return KDA_ERR_INVALID_ARG;
     return cache_copy(false, latent, pe, cu_seqlens, starts, T, B, dtype_o, c, stream);
 }
@@ -161,7 +164,7 @@ kda_status kda_mla_prefill(const void* q, const void* kv, const void* k_pe, cons
         !plain_dtype(dtype_qkv) || !plain_dtype(dtype_o) || !std::isfinite(softmax_scale))
         return KDA_ERR_INVALID_ARG;
     if (d_nope != kMlaNope || d_pe != kMlaPe || dv != kMlaV || dtype_qkv != KDA_BF16 || H > 65535 ||
-        Tq > 0x7fffffffLL || Tk > 0x7fffffffLL)
+        Tq > kMostRows || Tk > kMostRows)
         return KDA_ERR_UNSUPPORTED;
     if ((!cu_seqlens_q && Tq % B != 0) || (!cu_seqlens_k && Tk % B != 0)) return KDA_ERR_INVALID_ARG;
     if (Tq == 0) return KDA_OK;

@@ -2,6 +2,7 @@
 // e4m3 operands (kind::f16, kind::f8f6f4), untiled bulk copies, and bounded waits that end together.
 #pragma once
 
+#include "kda.h"
 #include "kda_common.cuh"
 #include "kda_sm100.cuh"
 
@@ -125,7 +126,7 @@ struct RoleWait {
     __device__ __forceinline__ bool aborted() const { return *abort_word != 0u; }
     __device__ __forceinline__ void give_up() const {
         *abort_word = 1u;
-        raise_flag(flags, 0x4u);
+        raise_flag(flags, KDA_DEVFLAG_TIMEOUT);
     }
     // For one thread: what it waits for is done (the others of its warp learn of a failure from it).
     __device__ __forceinline__ bool alone(uint64_t* bar, uint32_t parity) const {

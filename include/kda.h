@@ -279,8 +279,8 @@ KDA_API kda_status kda_decode_step_ex(const void* q, const void* k, const void* 
  *   page_table   [B, max_pages] int32 (device)     token j of sequence b lies in page page_table[b][j / page_size]
  *                                                  at row j % page_size.  Entries past a sequence's length are
  *                                                  not read.
- *   page_size a power of two from 16 to 1024; num_pages * page_size < 2^31; d_latent = 512, d_pe = 64
- *   (other sizes: KDA_ERR_UNSUPPORTED).
+ *   page_size a power of two from 16 to 1024; num_pages * page_size, max_pages * page_size and the packed rows T,
+ *   Tq, Tk at most 2^31 - 256; d_latent = 512, d_pe = 64 (other sizes: KDA_ERR_UNSUPPORTED).
  * cu_seqlens of these entry points: [B + 1] int32 (device) or NULL (equal lengths, T a multiple of B), as in
  * kda_chunk_fwd, but cu_seqlens[B] may be less than T: the rows behind it are neither read nor written.
  * What only the device can see (cu_seqlens, lengths, page numbers) raises KDA_DEVFLAG_CU_SEQLENS,

@@ -60,10 +60,30 @@ def test_decode_matches_the_definition(dtype, lengths, S, H, page):
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("lengths,S,H", [([70, 3], 40, 128), ([100], 1, 300), ([0, 130, 1], 37, 7)])
+def test_many_rows_per_sequence(dtype, lengths, S, H):
+    # from a few row tiles to more of them than SMs (then no sequence is split)
+    cache = Cache(lengths, 64, dtype, DEV).fill(2)
+    q, qp = _queries(len(lengths), S, H)
+    o, lse = _run(cache, q, qp, dtype_o=torch.float32)
+    _check(cache, q, qp, o, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
 def test_without_workspace(dtype):
     cache = Cache([3000, 0, 65, 129], 64, dtype, DEV).fill(2)
     q, qp = _queries(4, 1, 32)
     o, lse = _run(cache, q, qp, dtype_o=torch.float32, use_workspace=False)
+    _check(cache, q, qp, o, lse)
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+def test_more_sequences_than_threads(workspace):
+    g = torch.Generator().manual_seed(5)
+    lengths = [int(x) for x in torch.randint(0, 130, (1500,), generator=g)]
+    cache = Cache(lengths, 64, BF16, DEV).fill(4)
+    q, qp = _queries(1500, 1, 4)
+    o, lse = _run(cache, q, qp, dtype_o=torch.float32, use_workspace=workspace)
     _check(cache, q, qp, o, lse)
 
 

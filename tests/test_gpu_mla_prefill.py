@@ -78,6 +78,19 @@ def test_scores_that_rise_or_fall_by_hundreds(rising):
     check(lse, wl, lt, "lse")
 
 
+def test_many_short_sequences():
+    # more sequences than threads in a block, most of a few queries
+    g = torch.Generator().manual_seed(5)
+    nq = [int(x) for x in torch.randint(0, 9, (700,), generator=g)]
+    nk = [n + int(x) for n, x in zip(nq, torch.randint(0, 9, (700,), generator=g))]
+    nq[300], nk[300] = 400, 431
+    q, kv, kp = _inputs(sum(nq), sum(nk), 1)
+    o, lse = _run(q, kv, kp, nq, nk, dtype_o=torch.float32)
+    want, tol, wl, lt = mla_ref.prefill(q, kv, kp, nq, nk, True, SCALE, torch.float32)
+    check(o, want, tol, "o")
+    check(lse, wl, lt, "lse")
+
+
 def test_negative_and_zero_scale():
     q, kv, kp = _inputs(150, 150, 2)
     for scale in (0.0, -0.05):
