@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda.h"
 
 namespace kda {
@@ -149,6 +151,19 @@ struct MlaPrefillArgs {
     uint32_t wait_polls;
     cudaStream_t stream;
 };
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device, once per device (a bit each in `allowed`).
+template <typename K>
+inline cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& allowed) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
 
 cudaError_t launch_mla_cache_write(const MlaCacheCopyArgs& a);
 cudaError_t launch_mla_cache_read(const MlaCacheCopyArgs& a);

@@ -121,6 +121,18 @@ __host__ __device__ inline Part part_of(void* ws, int ctas, int R) {
     return p;
 }
 
+// x a / b for 0 <= a, b <= GROUPS; the 64-bit division, some 400 cycles of latency, only for what 32 bits do not hold.
+__device__ __forceinline__ long long scaled(long long x, int a, int b) {
+    if (x < (1 << 24)) return static_cast<uint32_t>(x) * static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return x * a / b;
+}
+// The largest group whose range begins at or before `place`: (place + 1) groups - 1 over total.
+__device__ __forceinline__ int group_of(long long place, int groups, long long total) {
+    const long long n = (place + 1) * groups - 1;
+    if (n < (1ll << 32)) return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(total));
+    return static_cast<int>(n / total);
+}
+
 // A CTA's walk over its range of tiles: one segment per sequence it touches.
 template <int LEAD>
 struct Walk {
@@ -238,8 +250,8 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         // no more ranges than tiles, so that none of those between a split sequence's first and last is empty
         if (total < groups) groups = static_cast<int>(total);
-        const long long first = total * group / groups;
-        const long long end = group < groups ? total * (group + 1) / groups : first;
+        const long long first = scaled(total, group, groups);
+        const long long end = group < groups ? scaled(total, group + 1, groups) : first;
         long long at = upto - mine;
         if (a.workspace) {  // cuts fall anywhere
             if (first < end && at <= first && first < upto) {
@@ -731,11 +743,6 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                     c.factor[h] = sum == 0.f ? 0.f : 1.f / sum;
                 }
-                if (!whole && tid == 0) {  // which groups share this sequence (group k's range begins at total k / G)
-                    const long long x = seg_w.t == 0 ? c.end - seg_w.n : c.first - seg_w.t;  // its first tile's place
-                    const auto group_of = [&](long long place) { return static_cast<int>(((place + 1) * groups - 1) / c.total); };
-                    part.meta[slot] = make_int4(seg_w.b, group_of(x), group_of(x + seg_w.nt - 1), 0);
-                }
                 group_sync(bar, 128);
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {  // 128 channels of this group's rows; thread = channel
@@ -790,6 +797,11 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < N; ++i) out[i * kMlaLatent] = o[i];
                     }
+                }
+                if (!whole && tid == 0) {  // which groups share this sequence (group k's range begins at total k / groups)
+                    const long long x = seg_w.t == 0 ? c.end - seg_w.n : c.first - seg_w.t;  // its first tile's place
+                    part.meta[slot] = make_int4(seg_w.b, group_of(x, groups, c.total),
+                                                group_of(x + seg_w.nt - 1, groups, c.total), 0);
                 }
                 tc_fence_before_sync();
                 group_sync(bar, 128);  // factor and red are free again
@@ -951,7 +963,8 @@ cudaError_t launch(const MlaDecodeArgs& a, const Grid& g) {
     using SH = Shape<R, E4M3>;
     constexpr int smem = kSmemBytes<R, E4M3>;
     auto kernel = mla_decode_kernel<R, E4M3, TO>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_shared(kernel, smem, allowed);
     if (err != cudaSuccess) return err;
     CUtensorMap q, qp, kv, pe;
     const int rows = a.S * a.H, box = a.cache.page_size < TOK ? a.cache.page_size : TOK;

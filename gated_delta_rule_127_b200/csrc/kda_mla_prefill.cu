@@ -435,7 +435,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 template <typename TO>
 cudaError_t launch(const MlaPrefillArgs& a) {
     auto kernel = mla_prefill_kernel<TO>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_shared(kernel, SMEM_BYTES, allowed);
     if (err != cudaSuccess) return err;
     // without keys nothing is loaded: any valid maps serve
     const bool none = a.Tk == 0;
