@@ -25,8 +25,13 @@
 // `go` for half of its weights, this tile's values and the other side's turn, `p_full` for the other half and the next
 // tile's keys.  A warp of its own reports the loads there (4,100 cycles with a look at each barrier).
 //
-// Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 loads (TMA), 9 and 10 issue the sides' products, 11
-// reports the loads' arrival.  Registers: 384 threads at 168 when launched, of which the last four warps give up 96 each so that the softmax
+// A CTA takes one item, 256 queries of a head, after another: the loads of the next one begin while the last tiles of
+// this one are computed, and its first scores while this one's output is written (about 14,000 cycles of an item that
+// would stand alone).  The grid has a block for every item; a running CTA takes over blocks that have not begun yet
+// (cluster launch control), so the hardware's order and balance stay.
+//
+// Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 finds the items and loads (TMA), 9 and 10 issue the
+// sides' products, 11 reports the loads' arrival.  Registers: 384 threads at 168 when launched, of which the last four warps give up 96 each so that the softmax
 // warps have 216 (a row's 128 scores): 256 x 216 + 128 x 72 = 384 x 168.
 #include <algorithm>
 
@@ -46,11 +51,25 @@ constexpr int OFF_RING = 2 * 3 * PIECE;                   // after both sides' q
 constexpr int OFF_CTL = OFF_RING + PIECES * PIECE;
 constexpr uint32_t COL_S = 0, COL_O = 256;                // tensor memory: per side 128 columns of each
 
+struct Item {                          // 256 queries of a head
+    int real;                          // 0: there are no more
+    int q0, k0, nq, nk;                // first rows and numbers of the sequence's queries and keys
+    int i0, head;                      // the first of the queries
+    // keys that the last query of a side sees, in tiles
+    __device__ __forceinline__ int tiles(int side, bool causal) const {
+        const int first = i0 + side * ROWS, last = min(first + ROWS, nq) - 1;
+        if (first >= nq) return 0;
+        const int see = causal ? min(max(last + 1 + nk - nq, 0), nk) : nk;
+        return (see + ROWS - 1) / ROWS;
+    }
+};
 struct Ctl {
-    uint64_t k_full[2], v_full[2], empty[PIECES], q_full[2], s_full[2], go[2], p_full[2], o_full[2], drain_bar[2];
+    alignas(16) uint4 taken;           // the answer of the launch control
+    uint64_t taken_full, item_full[2], item_empty[2];
+    uint64_t k_full[2], v_full[2], empty[PIECES], q_full[2], q_empty[2], s_full[2], go[2], p_full[2], zeroed[2], o_full[2],
+        o_empty[2], drain_bar[2];
+    Item item[2];
     uint32_t tmem, abort_word;
-    long long scan[THREADS / 32];
-    int b, pair;                       // this CTA's sequence (-1: none) and pair of query tiles
 };
 constexpr int SMEM_BYTES = OFF_CTL + static_cast<int>(sizeof(Ctl));
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -65,6 +84,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// Asks for a block of the grid that has not begun (the answer, 16 bytes, is counted on `bar`), and reads the answer:
+// true and its coordinates, or false, after which nothing is asked any more.
+__device__ __forceinline__ void ask_for_block(void* answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool block_taken(const void* answer, uint32_t& x, uint32_t& y) {
+    uint32_t got;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 z, w;\n\t"
+        "ld.shared.b128 h, [%3];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %2, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, z, w}, h;\n\t}\n"
+        : "+r"(x), "+r"(y), "=r"(got)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return got != 0u;
+}
+
 template <typename TO>
 __global__ void __launch_bounds__(THREADS, 1)
 mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -72,92 +114,69 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                    const __grid_constant__ MlaPrefillArgs a) {
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctl& c = *reinterpret_cast<Ctl*>(smem + OFF_CTL);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, head = blockIdx.y;
-
-    // ---- which 256 queries: pairs of query tiles are numbered over the sequences, the last pair of each (which sees the
-    // most keys) first
-    {
-        const int per = (a.B + THREADS - 1) / THREADS, lo = min(tid * per, a.B), hi = min(lo + per, a.B);
-        const auto pairs = [&](int b) {
-            int64_t first;
-            return (mla::seq_rows(a.cu_q, a.Tq, a.B, b, first, a.flags) + 2 * ROWS - 1) / (2 * ROWS);
-        };
-        long long mine = 0;
-        for (int b = lo; b < hi; ++b) mine += pairs(b);
-        long long upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += v;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        c.abort_word = 0u;
+        mbar_init(&c.taken_full, 1);
+        for (int i = 0; i < PIECES; ++i) mbar_init(&c.empty[i], 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.item_full[i], 1);
+            mbar_init(&c.item_empty[i], 11);  // all warps but the one that loads
+            mbar_init(&c.k_full[i], 1);
+            mbar_init(&c.v_full[i], 1);
+            mbar_init(&c.q_full[i], 1);
+            mbar_init(&c.q_empty[i], 1);
+            mbar_init(&c.s_full[i], 1);
+            mbar_init(&c.go[i], 6);
+            mbar_init(&c.p_full[i], 5);
+            mbar_init(&c.zeroed[i], 4);
+            mbar_init(&c.o_full[i], 1);
+            mbar_init(&c.o_empty[i], 4);
+            mbar_init(&c.drain_bar[i], 1);
         }
-        if (lane == 31) c.scan[warp] = upto;
-        if (tid == 0) {
-            c.abort_word = 0u;
-            c.b = -1;
-            for (int i = 0; i < PIECES; ++i) mbar_init(&c.empty[i], 2);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&c.q_full[i], 1);
-                mbar_init(&c.s_full[i], 1);
-                mbar_init(&c.go[i], 6);
-                mbar_init(&c.p_full[i], 5);
-                mbar_init(&c.o_full[i], 1);
-                mbar_init(&c.k_full[i], 1);
-                mbar_init(&c.v_full[i], 1);
-                mbar_init(&c.drain_bar[i], 1);
-            }
-            fence_mbar_init();
-        }
-        if (warp == 9) tmem_alloc(&c.tmem, 512);
-        if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_q : lane == 1 ? &tm_k : lane == 2 ? &tm_v : &tm_pe);
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += c.scan[w];
-        long long at = upto - mine;
-        if (at <= blockIdx.x && blockIdx.x < upto) {
-            int b = lo;
-            while (blockIdx.x >= at + pairs(b)) at += pairs(b++);
-            c.b = b;
-            c.pair = pairs(b) - 1 - static_cast<int>(blockIdx.x - at);
-        }
-        tc_fence_before_sync();
-        __syncthreads();
-        tc_fence_after_sync();
+        fence_mbar_init();
     }
+    if (warp == 9) tmem_alloc(&c.tmem, 512);
+    if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_q : lane == 1 ? &tm_k : lane == 2 ? &tm_v : &tm_pe);
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        mla::check_cu(a.cu_q, a.Tq, a.B, a.flags);
+        mla::check_cu(a.cu_k, a.Tk, a.B, a.flags);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
     const uint32_t tmem = c.tmem;
     const RoleWait wait{a.wait_polls, &c.abort_word, a.flags};
 
-    if (c.b >= 0) {
-        int64_t q0, k0;
-        const int nq = mla::seq_rows(a.cu_q, a.Tq, a.B, c.b, q0, a.flags);
-        const int nk = mla::seq_rows(a.cu_k, a.Tk, a.B, c.b, k0, a.flags);
-        const int i0 = c.pair * 2 * ROWS;
-        // keys that the last query of a side sees, and tiles of them
-        const auto tiles = [&](int side) {
-            const int first = i0 + side * ROWS, last = min(first + ROWS, nq) - 1;
-            if (first >= nq) return 0;
-            const int see = a.causal ? min(max(last + 1 + nk - nq, 0), nk) : nk;
-            return (see + ROWS - 1) / ROWS;
-        };
-        const int n0 = tiles(0), n1 = tiles(1), most = max(n0, n1);
-
-        if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-            // ---------------------------------------------------------------- softmax and output of one side
-            const int s = warp >> 2, n = s == 0 ? n0 : n1;
-            const int i = i0 + s * ROWS + (warp & 3) * 32 + lane;  // this thread's query
-            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const uint32_t at_s = tmem + lanes + COL_S + s * 128, at_o = tmem + lanes + COL_O + s * 128;
-            // the last key that the query sees, and a scale that is never 0 or negative (scores are negated instead)
-            const int see = i < nq ? (a.causal ? min(i + nk - nq, nk - 1) : nk - 1) : -1;
+    // Every role counts on across the items: tiles (jt), steps of a side (st), its items with keys (outs).  Phases of a
+    // barrier are numbered by these counts.
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // -------------------------------------------------------------------- softmax and output of one side
+        const int s = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t at_s = tmem + lanes + COL_S + s * 128, at_o = tmem + lanes + COL_O + s * 128;
+        // a scale that is never 0 or negative (scores are negated instead)
+        const float sl2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        const bool negate = a.scale < 0.f;
+        uint32_t it = 0, jt = 0, st = 0, outs = 0, ends = 0;
+        bool ok = true;
+        while (true) {
+            ok = wait(&c.item_full[it & 1], (it >> 1) & 1);
+            if (!ok) break;
+            const Item w = c.item[it & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.item_empty[it & 1]);
+            ++it;
+            if (!w.real) break;
+            const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), n = s == 0 ? n0 : n1, nk = w.nk;
+            const int i = w.i0 + s * ROWS + (warp & 3) * 32 + lane;  // this thread's query
+            // the last key that the query sees
+            const int see = i < w.nq ? (a.causal ? min(i + nk - w.nq, nk - 1) : nk - 1) : -1;
             const int warp_see = __reduce_min_sync(0xffffffffu, see);  // by the warp's query that sees least
-            const float sl2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-            const bool negate = a.scale < 0.f;
             float m = -INFINITY, l = 0.f;
-            // the tile that the sequence ends in, if any (then it is the side's last): all four warps meet there, once,
-            // also those whose waits have failed
-            const int ending = n * ROWS > nk ? n - 1 : -1;
-            bool ok = true, met = ending < 0;
-            for (int j = 0; j < n; ++j) {
-                ok = wait(&c.s_full[s], j & 1);
+            for (int j = 0; j < n; ++j, ++st) {
+                ok = wait(&c.s_full[s], st & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t raw[4][32];
@@ -180,21 +199,25 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int k = 0; k < ROWS; ++k)
                         if (k > left) x[k] = -INFINITY;
                 }
-                if (j == ending) {
+                if (j * ROWS + ROWS > nk) {
                     // rows of V past the sequence's end hold whatever lies there: zero them, so that their weight of 0
-                    // meets no NaN (both sides do, each before its own product)
-                    const uint32_t g = j * PER_TILE + 3;
-                    ok = wait(&c.v_full[j & 1], (j >> 1) & 1);
+                    // meets no NaN (both sides do, each before its own product, all four warps before any of them
+                    // announces weights)
+                    const uint32_t g = (jt + j) * PER_TILE + 3;
+                    ok = wait(&c.v_full[(jt + j) & 1], ((jt + j) >> 1) & 1);
+                    if (!ok) break;
                     const int r = (warp & 3) * 32 + lane;  // a key of the tile
-                    if (ok && r >= nk - j * ROWS) {
+                    if (r >= nk - j * ROWS) {
                         unsigned char* v = smem + OFF_RING + ((g + (r >> 6)) % PIECES) * PIECE + (r & 63) * 128;
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             *reinterpret_cast<uint4*>(v + (k >> 3) * (PIECE / 2) + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
-                    ok = !group_sync_or(1 + s, 128, !ok);  // zeroed before any warp's weights are announced
-                    met = true;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.zeroed[s]);
+                    ok = wait(&c.zeroed[s], ends & 1);
+                    ++ends;
                     if (!ok) break;
                 }
                 float t[4] = {x[0], x[1], x[2], x[3]};
@@ -243,12 +266,16 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
-            if (!met) group_sync_or(1 + s, 128, true);
-            if (n > 0 && ok) ok = wait(&c.o_full[s], 0);
-            if (ok && i0 + s * ROWS < nq) {
+            if (!ok) break;
+            if (n > 0) {
+                ok = wait(&c.o_full[s], outs & 1);
+                if (!ok) break;
+                ++outs;
                 tc_fence_after_sync();
+            }
+            if (w.i0 + s * ROWS < w.nq) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int64_t row = (q0 + i) * a.H + head;
+                const int64_t row = (static_cast<int64_t>(w.q0) + i) * a.H + w.head;
                 TO* out = static_cast<TO*>(a.o) + row * kMlaV;
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
@@ -259,7 +286,12 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
                     }
-                    if (i < nq) {
+                    if (n > 0 && k == 3) {  // read: the next item's first product may overwrite it
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.o_empty[s]);
+                    }
+                    if (i < w.nq) {
                         if constexpr (sizeof(TO) == 2) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -274,105 +306,187 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                     }
                 }
-                if (a.lse && i < nq) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+                if (a.lse && i < w.nq) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
             }
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-            if (warp == 8) {
-                // ---------------------------------------------------------------- loads
-                uint32_t g = 0;
-                bool ok = true;
-                if (most > 0 && elect_one()) {
+            jt += max(n0, n1);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            // ---------------------------------------------------------------- items and loads
+            uint32_t it = 0, g = 0, asked = 0, answered = 0, qn[2] = {0, 0};
+            uint32_t x = blockIdx.x, y = blockIdx.y;
+            int row = 0;                    // of the tile being loaded
+            int32_t scan_b = 0;             // sequences before it have `scan_at` pairs of query tiles
+            uint32_t scan_at = 0;
+            bool ok = true, more = true;
+            const auto pairs = [&](int b) {
+                int64_t first;
+                return b < a.B ? (mla::seq_rows(a.cu_q, a.Tq, a.B, b, first, a.flags) + 2 * ROWS - 1) / (2 * ROWS) : 0;
+            };
+            while (ok) {
+                // block x is pair number x of query tiles, numbered over the sequences, the last pair of each (which sees the
+                // most keys) first; the grid may have more blocks than there are pairs
+                Item w{};
+                if (x < scan_at) scan_b = scan_at = 0;
+                while (more && scan_b < a.B && !w.real) {
+                    const int p = pairs(scan_b + lane);
+                    int upto = p;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+                        if (lane >= d) upto += v;
+                    }
+                    const uint32_t has = __ballot_sync(0xffffffffu, x < scan_at + upto);
+                    if (has) {
+                        const int l = __ffs(has) - 1, b = scan_b + l;
+                        const int mine = __shfl_sync(0xffffffffu, p, l), before = __shfl_sync(0xffffffffu, upto, l) - mine;
+                        int64_t first;
+                        w.real = 1;
+                        w.nq = mla::seq_rows(a.cu_q, a.Tq, a.B, b, first, a.flags);
+                        w.q0 = static_cast<int>(first);
+                        w.nk = mla::seq_rows(a.cu_k, a.Tk, a.B, b, first, a.flags);
+                        w.k0 = static_cast<int>(first);
+                        w.i0 = (mine - 1 - static_cast<int>(x - scan_at - before)) * 2 * ROWS;
+                        w.head = y;
+                    } else {
+                        scan_at += __shfl_sync(0xffffffffu, upto, 31);
+                        scan_b += 32;
+                    }
+                }
+                if (w.real || !more) {  // told to the other roles: an item, or that there are no more
+                    ok = wait(&c.item_empty[it & 1], ((it >> 1) & 1) ^ 1);
+                    if (!ok) break;
+                    if (!more) w.real = 0;
+                    if (lane == 0) {
+                        c.item[it & 1] = w;
+                        mbar_arrive(&c.item_full[it & 1]);
+                    }
+                    __syncwarp();
+                    ++it;
+                }
+                if (!more) break;
+                if (elect_one()) ask_for_block(&c.taken, &c.taken_full);
+                __syncwarp();
+                ++asked;
+                if (w.real) {
+                    const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), most = max(n0, n1);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if ((s == 0 ? n0 : n1) == 0) continue;
-                        mbar_arrive_expect_tx(&c.q_full[s], 3 * PIECE);
+                        ok = ok && wait(&c.q_empty[s], (qn[s] & 1) ^ 1);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&c.q_full[s], 3 * PIECE);
 #pragma unroll
-                        for (int k = 0; k < 3; ++k)
-                            tma_load_3d(smem + (s * 3 + k) * PIECE, &tm_q, k * 64, head, static_cast<int>(q0) + i0 + s * ROWS,
-                                        &c.q_full[s]);
+                            for (int k = 0; k < 3; ++k)
+                                tma_load_3d(smem + (s * 3 + k) * PIECE, &tm_q, k * 64, w.head, w.q0 + w.i0 + s * ROWS, &c.q_full[s]);
+                        }
+                        __syncwarp();
+                        ++qn[s];
+                    }
+                    for (int j = 0; j < most && ok; ++j) {
+                        const uint32_t jt = g / PER_TILE;
+                        row = w.k0 + j * ROWS;
+                        uint64_t *kb = &c.k_full[jt & 1], *vb = &c.v_full[jt & 1];
+#pragma unroll
+                        for (int k = 0; k < PER_TILE; ++k) {
+                            const uint32_t slot = g % PIECES;
+                            ok = wait(&c.empty[slot], ((g / PIECES) & 1) ^ 1);
+                            if (!ok) break;
+                            if (elect_one()) {
+                                unsigned char* dst = smem + OFF_RING + slot * PIECE;
+                                if (k == 0) mbar_arrive_expect_tx(kb, 3 * PIECE);
+                                if (k == 3) mbar_arrive_expect_tx(vb, 2 * PIECE);
+                                if (k < 2) {
+                                    tma_load_3d(dst, &tm_k, k * 64, w.head, row, kb);
+                                } else if (k == 2) {
+                                    tma_load_3d(dst, &tm_pe, 0, 0, row, kb);
+                                } else {
+                                    tma_load_3d(dst, &tm_v, kMlaNope, w.head, row + (k - 3) * 64, vb);
+                                    tma_load_3d(dst + PIECE / 2, &tm_v, kMlaNope + 64, w.head, row + (k - 3) * 64, vb);
+                                }
+                            }
+                            __syncwarp();
+                            ++g;
+                        }
+                    }
+                }
+                ok = ok && wait(&c.taken_full, answered & 1);
+                if (!ok) break;
+                ++answered;
+                more = block_taken(&c.taken, x, y);
+                fence_async_smem();  // read before the next answer is written there
+                __syncwarp();
+            }
+            if (!ok) {
+                // let what is in flight land before the block ends; first what a begun group of pieces still lacks, or its
+                // barrier would never complete
+                const int j = g / PER_TILE, k = g % PER_TILE;
+                if (k != 0 && k != 3 && elect_one()) {
+                    for (int i = k; i < (k < 3 ? 3 : 5); ++i) {
+                        uint64_t* b = k < 3 ? &c.k_full[j & 1] : &c.v_full[j & 1];
+                        unsigned char* dst = smem + OFF_RING + (g - k + i) % PIECES * PIECE;
+                        tma_load_3d(dst, &tm_pe, 0, 0, row, b);  // any piece of this size: nobody reads it
                     }
                 }
                 __syncwarp();
-                for (int j = 0; j < most && ok; ++j) {
-                    const int row = static_cast<int>(k0) + j * ROWS;
-                    uint64_t *kb = &c.k_full[j & 1], *vb = &c.v_full[j & 1];
+                const int last_k = j - (k > 0 ? 0 : 1), last_v = j - (k > 3 ? 0 : 1);  // last tiles begun
+                for (int i = max(last_k - 1, 0); i <= last_k; ++i) drain(&c.k_full[i & 1], (i >> 1) & 1);
+                for (int i = max(last_v - 1, 0); i <= last_v; ++i) drain(&c.v_full[i & 1], (i >> 1) & 1);
+                for (int s = 0; s < 2; ++s)
+                    if (qn[s] > 0) drain(&c.q_full[s], (qn[s] - 1) & 1);
+                if (asked > answered) drain(&c.taken_full, answered & 1);
+            }
+        } else if (warp == 9 || warp == 10) {
+            // ---------------------------------------------------------------- products of one side
+            const int s = warp - 9;
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
+            const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
+            constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
+            if (elect_one()) {
+                const auto scores = [&](uint32_t g, bool last) {
+                    tc_fence_after_sync();
 #pragma unroll
-                    for (int k = 0; k < PER_TILE; ++k) {
-                        const uint32_t slot = g % PIECES;
-                        ok = wait(&c.empty[slot], ((g / PIECES) & 1) ^ 1);
+                    for (int k = 0; k < 3; ++k) {
+                        const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
+                    }
+                    mma_commit(&c.s_full[s]);
+                    if (last) mma_commit(&c.q_empty[s]);
+                };
+                const auto release = [&](uint32_t g, int count) {
+                    for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
+                };
+                uint32_t it = 0, jt = 0, st = 0, outs = 0;
+                bool ok = true;
+                while (true) {
+                    ok = wait.alone(&c.item_full[it & 1], (it >> 1) & 1);
+                    if (!ok) break;
+                    const Item w = c.item[it & 1];
+                    mbar_arrive(&c.item_empty[it & 1]);
+                    ++it;
+                    if (!w.real) break;
+                    const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), n = s == 0 ? n0 : n1, most = max(n0, n1);
+                    uint32_t g = jt * PER_TILE;
+                    if (n > 0) {
+                        ok = wait.alone(&c.q_full[s], outs & 1) && wait.alone(&c.k_full[jt & 1], (jt >> 1) & 1);
                         if (!ok) break;
-                        if (elect_one()) {
-                            unsigned char* dst = smem + OFF_RING + slot * PIECE;
-                            if (k == 0) mbar_arrive_expect_tx(kb, 3 * PIECE);
-                            if (k == 3) mbar_arrive_expect_tx(vb, 2 * PIECE);
-                            if (k < 2) {
-                                tma_load_3d(dst, &tm_k, k * 64, head, row, kb);
-                            } else if (k == 2) {
-                                tma_load_3d(dst, &tm_pe, 0, 0, row, kb);
-                            } else {
-                                tma_load_3d(dst, &tm_v, kMlaNope, head, row + (k - 3) * 64, vb);
-                                tma_load_3d(dst + PIECE / 2, &tm_v, kMlaNope + 64, head, row + (k - 3) * 64, vb);
-                            }
-                        }
-                        __syncwarp();
-                        ++g;
+                        scores(g, n == 1);
+                        release(g, 3);
+                        ok = outs == 0 || wait.alone(&c.o_empty[s], (outs - 1) & 1);  // the last item's output has been read
+                        ++outs;
                     }
-                }
-                if (!ok) {
-                    // let what is in flight land before the block ends; first what a begun group of pieces still lacks, or its
-                    // barrier would never complete
-                    const int j = g / PER_TILE, k = g % PER_TILE;
-                    if (k != 0 && k != 3 && elect_one()) {
-                        const int row = static_cast<int>(k0) + j * ROWS;
-                        for (int i = k; i < (k < 3 ? 3 : 5); ++i) {
-                            uint64_t* b = k < 3 ? &c.k_full[j & 1] : &c.v_full[j & 1];
-                            unsigned char* dst = smem + OFF_RING + (g - k + i) % PIECES * PIECE;
-                            tma_load_3d(dst, &tm_pe, 0, 0, row, b);  // any piece of this size: nobody reads it
-                        }
-                    }
-                    __syncwarp();
-                    const int last_k = j - (k > 0 ? 0 : 1), last_v = j - (k > 3 ? 0 : 1);  // last tiles begun
-                    for (int i = max(last_k - 1, 0); i <= last_k; ++i) drain(&c.k_full[i & 1], (i >> 1) & 1);
-                    for (int i = max(last_v - 1, 0); i <= last_v; ++i) drain(&c.v_full[i & 1], (i >> 1) & 1);
-                    if (n0 > 0) drain(&c.q_full[0], 0);
-                    if (n1 > 0) drain(&c.q_full[1], 0);
-                }
-            } else if (warp == 9 || warp == 10) {
-                // ---------------------------------------------------------------- products of one side
-                const int s = warp - 9, n = s == 0 ? n0 : n1;
-                const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-                const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
-                const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
-                constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
-                if (elect_one()) {
-                    const auto scores = [&](uint32_t g) {
-                        tc_fence_after_sync();
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
-                        }
-                        mma_commit(&c.s_full[s]);
-                    };
-                    const auto release = [&](uint32_t g, int count) {
-                        for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
-                    };
-                    bool ok = n == 0 || (wait.alone(&c.q_full[s], 0) && wait.alone(&c.k_full[0], 0));
-                    if (ok && n > 0) {
-                        scores(0);
-                        release(0, 3);
-                    }
-                    uint32_t g = 0;
-                    for (int j = 0; j < n && ok; ++j, g += PER_TILE) {
+                    for (int j = 0; j < n && ok; ++j, ++st, g += PER_TILE) {
                         if (s == 0 ? j == 0 || j > n1 : j >= n0) mbar_arrive(&c.go[s]);  // no other side to wait for
-                        ok = wait.alone(&c.go[s], j & 1);
+                        ok = wait.alone(&c.go[s], st & 1);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (k == 1) ok = ok && wait.alone(&c.p_full[s], j & 1);
+                            if (k == 1) ok = ok && wait.alone(&c.p_full[s], st & 1);
                             if (!ok) break;
                             tc_fence_after_sync();
                             const uint64_t vd = sw128_desc(base + OFF_RING + (g + 3 + k) % PIECES * PIECE, PIECE / 2, 1024);
@@ -382,46 +496,61 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             release(g + 3 + k, 1);  // before the scores: what a commit reports is all that came before it
                         }
                         if (!ok) break;
-                        if (j + 1 < n) scores(g + PER_TILE);
+                        if (j + 1 < n) scores(g + PER_TILE, j + 2 == n);
                         if (s == 0 ? j < n1 : j + 1 < n0) mbar_arrive(&c.go[s ^ 1]);  // the other side's turn
                         if (j + 1 < n) release(g + PER_TILE, 3);
                         else mma_commit(&c.o_full[s]);
                     }
                     for (int j = n; j < most && ok; ++j, g += PER_TILE) {  // keys that only the other side sees
-                        ok = wait.alone(&c.k_full[j & 1], (j >> 1) & 1);
+                        const uint32_t t = jt + j;
+                        ok = wait.alone(&c.k_full[t & 1], (t >> 1) & 1);
                         for (int k = 0; k < 3 && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
-                        ok = ok && wait.alone(&c.v_full[j & 1], (j >> 1) & 1);
+                        ok = ok && wait.alone(&c.v_full[t & 1], (t >> 1) & 1);
                         for (int k = 3; k < PER_TILE && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
                     }
-                    if (!ok) {  // let issued products finish before the block ends
-                        mma_commit(&c.drain_bar[s]);
-                        drain(&c.drain_bar[s], 0);
-                    }
+                    if (!ok) break;
+                    jt += most;
                 }
-                __syncwarp();
-            } else {
-                // ---------------------------------------------------------------- arrivals: tells the sides' steps of them
-                if (elect_one()) {
-                    bool ok = true;
-                    for (int j = 0; j < most && ok; ++j) {
-                        ok = wait.alone(&c.v_full[j & 1], (j >> 1) & 1);
+                if (!ok) {  // let issued products finish before the block ends
+                    mma_commit(&c.drain_bar[s]);
+                    drain(&c.drain_bar[s], 0);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ---------------------------------------------------------------- arrivals: tells the sides' steps of them
+            if (elect_one()) {
+                uint32_t it = 0, jt = 0, st[2] = {0, 0};
+                bool ok = true;
+                while (true) {
+                    ok = wait.alone(&c.item_full[it & 1], (it >> 1) & 1);
+                    if (!ok) break;
+                    const Item w = c.item[it & 1];
+                    mbar_arrive(&c.item_empty[it & 1]);
+                    ++it;
+                    if (!w.real) break;
+                    const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), most = max(n0, n1);
+                    for (int j = 0; j < most && ok; ++j, ++jt) {
+                        ok = wait.alone(&c.v_full[jt & 1], (jt >> 1) & 1);
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {  // one step at a time, here and below
                             if (j >= (s == 0 ? n0 : n1)) continue;
-                            ok = ok && (j == 0 || wait.alone(&c.go[s], (j - 1) & 1));
+                            ok = ok && (st[s] == 0 || wait.alone(&c.go[s], (st[s] - 1) & 1));
                             if (ok) mbar_arrive(&c.go[s]);
                         }
-                        if (j + 1 < most) ok = ok && wait.alone(&c.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+                        if (j + 1 < most) ok = ok && wait.alone(&c.k_full[(jt + 1) & 1], ((jt + 1) >> 1) & 1);
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             if (j >= (s == 0 ? n0 : n1)) continue;
-                            ok = ok && (j == 0 || wait.alone(&c.p_full[s], (j - 1) & 1));
+                            ok = ok && (st[s] == 0 || wait.alone(&c.p_full[s], (st[s] - 1) & 1));
                             if (ok) mbar_arrive(&c.p_full[s]);
+                            ++st[s];
                         }
                     }
+                    if (!ok) break;
                 }
-                __syncwarp();
             }
+            __syncwarp();
         }
     }
     tc_fence_before_sync();
