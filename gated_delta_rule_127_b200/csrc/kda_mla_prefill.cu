@@ -8,7 +8,7 @@
 //
 // The sides take turns on the tensor core: while one side's scores become weights (four warps, thread = row, its 128
 // scores in registers), the other side's products run.  Scores and outputs of both sides fill the 512 columns of
-// tensor memory; the weights are written over the scores they come from, in bf16, and are the second product's A
+// tensor memory; the weights are written over scores that have been read, in bf16, and are the second product's A
 // operand there.  Per tile and side the tensor core needs 1,280 cycles (128 x 128 x (192 + 128) products at 4,096 a
 // cycle), the exponentials 1,024 cycles of the special-function units, so the two are meant to overlap.
 //
@@ -31,8 +31,7 @@
 // (cluster launch control), so the hardware's order and balance stay.
 //
 // Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 finds the items and loads (TMA), 9 and 10 issue the
-// sides' products, 11 reports the loads' arrival.  Registers: 384 threads at 168 when launched, of which the last four warps give up 96 each so that the softmax
-// warps have 216 (a row's 128 scores): 256 x 216 + 128 x 72 = 384 x 168.
+// sides' products, 11 reports the loads' arrival.
 #include <algorithm>
 
 #include "kda_mla_common.cuh"
@@ -151,14 +150,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // Every role counts on across the items: tiles (jt), steps of a side (st), its items with keys (outs).  Phases of a
     // barrier are numbered by these counts.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // -------------------------------------------------------------------- softmax and output of one side
         const int s = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t at_s = tmem + lanes + COL_S + s * 128, at_o = tmem + lanes + COL_O + s * 128;
-        // a scale that is never 0 or negative (scores are negated instead)
-        const float sl2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        // the scale in log2 units, never 0: a hidden score, infinite of the other sign, gives a weight of 0
         const bool negate = a.scale < 0.f;
+        const float sl2 = copysignf(fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f), negate ? -1.f : 1.f);
+        const uint32_t hidden = negate ? 0x7F800000u : 0xFF800000u;
         uint32_t it = 0, jt = 0, st = 0, outs = 0, ends = 0;
         bool ok = true;
         while (true) {
@@ -171,33 +170,50 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!w.real) break;
             const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), n = s == 0 ? n0 : n1, nk = w.nk;
             const int i = w.i0 + s * ROWS + (warp & 3) * 32 + lane;  // this thread's query
-            // the last key that the query sees
-            const int see = i < w.nq ? (a.causal ? min(i + nk - w.nq, nk - 1) : nk - 1) : -1;
+            // the last key that the query sees (one past the sequence's end, never stored, as the last query does)
+            const int see = a.causal ? min(i + nk - w.nq, nk - 1) : nk - 1;
             const int warp_see = __reduce_min_sync(0xffffffffu, see);  // by the warp's query that sees least
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j, ++st) {
                 ok = wait(&c.s_full[s], st & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
-                uint32_t raw[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32_nw(at_s + k * 32, raw[k]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) after_ld_wait(raw[k]);
-                float x[ROWS];
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k) x[k] = __uint_as_float(raw[k >> 5][k & 31]);
-                if (negate) {
-#pragma unroll
-                    for (int k = 0; k < ROWS; ++k) x[k] = -x[k];
-                }
+                // The 128 scores in two passes of four quarters, each read from tensor memory while the one before is worked
+                // on; the loops stay loops, which keeps the code in the instruction caches (fully unrolled, with all
+                // scores in registers, warps stood without instructions a fifth of the time).
                 const bool edge = j * ROWS + ROWS - 1 > warp_see;  // some query of the warp does not see the whole tile
-                if (edge) {
-                    const int left = see - j * ROWS;   // the last column this one sees
+                uint32_t xa[32], xb[32];
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const auto look = [&](uint32_t (&x)[32], int col) {
+                    if (edge) {  // hidden scores are written back as such for the second pass
+                        const int left = see - j * ROWS - col;  // the last column that this query sees
 #pragma unroll
-                    for (int k = 0; k < ROWS; ++k)
-                        if (k > left) x[k] = -INFINITY;
+                        for (int k = 0; k < 32; ++k)
+                            if (k > left) x[k] = hidden;
+                        tmem_st32_nw(at_s + col, x);
+                        tmem_st_wait();
+                    }
+                    if (negate) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], -__uint_as_float(x[k]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(x[k]));
+                    }
+                };
+                tmem_ld32_nw(at_s, xa);
+                tmem_ld_wait();
+                after_ld_wait(xa);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld32_nw(at_s + h * 64 + 32, xb);
+                    look(xa, h * 64);
+                    tmem_ld_wait();
+                    after_ld_wait(xb);
+                    tmem_ld32_nw(at_s + (h == 0 ? 64 : 0), xa);  // at last the second pass's first quarter
+                    look(xb, h * 64 + 32);
+                    tmem_ld_wait();
+                    after_ld_wait(xa);
                 }
                 if (j * ROWS + ROWS > nk) {
                     // rows of V past the sequence's end hold whatever lies there: zero them, so that their weight of 0
@@ -220,10 +236,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++ends;
                     if (!ok) break;
                 }
-                float t[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int k = 4; k < ROWS; ++k) t[k & 3] = fmaxf(t[k & 3], x[k]);
-                const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * sl2;
+                const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fabsf(sl2);
                 const bool move = top > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
                     float f = 1.f;
@@ -245,25 +258,40 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[16];
+                uint32_t w16[16];
+                const auto weigh = [&](const uint32_t (&x)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float u = ex2(fmaf(x[k * 32 + e], sl2, -ref)), v = ex2(fmaf(x[k * 32 + e + 1], sl2, -ref));
+                        const float u = ex2(fmaf(__uint_as_float(x[e]), sl2, -ref)), v = ex2(fmaf(__uint_as_float(x[e + 1]), sl2, -ref));
                         sum[e & 2] += u;
                         sum[(e & 2) + 1] += v;
-                        w[e / 2] = pack_bf16(u, v);
+                        w16[e / 2] = pack_bf16(u, v);
                     }
-                    if (k == 3) tmem_st16_nw(at_s + k * 16, w);
-                    if (k >= 2) {  // the first half is announced when the third quarter has been computed: its stores have landed
-                        tmem_st_wait();
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(k == 2 ? &c.go[s] : &c.p_full[s]);
+                };
+                const auto announce = [&](uint64_t* bar) {
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                // a quarter's weights go over scores that have been read: columns 16 k .. of quarter k / 2
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld32_nw(at_s + h * 64 + 32, xb);
+                    weigh(xa);
+                    if (h == 1) announce(&c.go[s]);  // the first half: its stores have long landed
+                    tmem_st16_nw(at_s + h * 32, w16);
+                    tmem_ld_wait();
+                    after_ld_wait(xb);
+                    if (h == 0) tmem_ld32_nw(at_s + 64, xa);
+                    weigh(xb);
+                    tmem_st16_nw(at_s + h * 32 + 16, w16);
+                    if (h == 0) {
+                        tmem_ld_wait();
+                        after_ld_wait(xa);
                     }
-                    if (k < 3) tmem_st16_nw(at_s + k * 16, w);
                 }
+                announce(&c.p_full[s]);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
             if (!ok) break;
@@ -311,7 +339,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             jt += max(n0, n1);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
             // ---------------------------------------------------------------- items and loads
             uint32_t it = 0, g = 0, asked = 0, answered = 0, qn[2] = {0, 0};
@@ -371,11 +398,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++asked;
                 if (w.real) {
                     const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), most = max(n0, n1);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if ((s == 0 ? n0 : n1) == 0) continue;
-                        ok = ok && wait(&c.q_empty[s], (qn[s] & 1) ^ 1);
-                        if (!ok) break;
+                    const auto queries = [&](int s) {
+                        if (!wait(&c.q_empty[s], (qn[s] & 1) ^ 1)) return false;
                         if (elect_one()) {
                             mbar_arrive_expect_tx(&c.q_full[s], 3 * PIECE);
 #pragma unroll
@@ -384,7 +408,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         __syncwarp();
                         ++qn[s];
-                    }
+                        return true;
+                    };
+                    if (n0 > 0) ok = queries(0);
                     for (int j = 0; j < most && ok; ++j) {
                         const uint32_t jt = g / PER_TILE;
                         row = w.k0 + j * ROWS;
@@ -392,7 +418,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                         for (int k = 0; k < PER_TILE; ++k) {
                             const uint32_t slot = g % PIECES;
-                            ok = wait(&c.empty[slot], ((g / PIECES) & 1) ^ 1);
+                            // the second side is half a step behind: its queries come after the first keys
+                            if (k == 3 && j == 0 && n1 > 0) ok = queries(1);
+                            ok = ok && wait(&c.empty[slot], ((g / PIECES) & 1) ^ 1);
                             if (!ok) break;
                             if (elect_one()) {
                                 unsigned char* dst = smem + OFF_RING + slot * PIECE;
@@ -446,111 +474,117 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
             const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
             constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
-            if (elect_one()) {
-                const auto scores = [&](uint32_t g, bool last) {
-                    tc_fence_after_sync();
+            // Whole warps wait, one lane issues.
+            const auto scores = [&](uint32_t g, bool last) {
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
+                for (int k = 0; k < 3; ++k) {
+                    const uint64_t kd = sw128_desc(base + OFF_RING + (g + k) % PIECES * PIECE, 16, 1024);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
-                    }
-                    mma_commit(&c.s_full[s]);
-                    if (last) mma_commit(&c.q_empty[s]);
-                };
-                const auto release = [&](uint32_t g, int count) {
-                    for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
-                };
-                uint32_t it = 0, jt = 0, st = 0, outs = 0;
-                bool ok = true;
-                while (true) {
-                    ok = wait.alone(&c.item_full[it & 1], (it >> 1) & 1);
+                    for (int i = 0; i < 4; ++i)
+                        mma_f16(d_s, q + ((k * PIECE + i * 32) >> 4), kd + i * 2, idesc_s, k + i > 0);
+                }
+                mma_commit(&c.s_full[s]);
+                if (last) mma_commit(&c.q_empty[s]);
+            };
+            const auto release = [&](uint32_t g, int count) {
+                for (int k = 0; k < count; ++k) mma_commit(&c.empty[(g + k) % PIECES]);
+            };
+            uint32_t it = 0, jt = 0, st = 0, outs = 0;
+            bool ok = true;
+            while (true) {
+                ok = wait(&c.item_full[it & 1], (it >> 1) & 1);
+                if (!ok) break;
+                const Item w = c.item[it & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.item_empty[it & 1]);
+                ++it;
+                if (!w.real) break;
+                const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), n = s == 0 ? n0 : n1, most = max(n0, n1);
+                uint32_t g = jt * PER_TILE;
+                if (n > 0) {
+                    ok = wait(&c.q_full[s], outs & 1) && wait(&c.k_full[jt & 1], (jt >> 1) & 1);
                     if (!ok) break;
-                    const Item w = c.item[it & 1];
-                    mbar_arrive(&c.item_empty[it & 1]);
-                    ++it;
-                    if (!w.real) break;
-                    const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), n = s == 0 ? n0 : n1, most = max(n0, n1);
-                    uint32_t g = jt * PER_TILE;
-                    if (n > 0) {
-                        ok = wait.alone(&c.q_full[s], outs & 1) && wait.alone(&c.k_full[jt & 1], (jt >> 1) & 1);
-                        if (!ok) break;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
                         scores(g, n == 1);
                         release(g, 3);
-                        ok = outs == 0 || wait.alone(&c.o_empty[s], (outs - 1) & 1);  // the last item's output has been read
-                        ++outs;
                     }
-                    for (int j = 0; j < n && ok; ++j, ++st, g += PER_TILE) {
-                        if (s == 0 ? j == 0 || j > n1 : j >= n0) mbar_arrive(&c.go[s]);  // no other side to wait for
-                        ok = wait.alone(&c.go[s], st & 1);
+                    __syncwarp();
+                    ok = outs == 0 || wait(&c.o_empty[s], (outs - 1) & 1);  // the last item's output has been read
+                    ++outs;
+                }
+                for (int j = 0; j < n && ok; ++j, ++st, g += PER_TILE) {
+                    if ((s == 0 ? j == 0 || j > n1 : j >= n0) && lane == 0) mbar_arrive(&c.go[s]);  // no other side to wait for
+                    __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (k == 1) ok = ok && wait.alone(&c.p_full[s], st & 1);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            const uint64_t vd = sw128_desc(base + OFF_RING + (g + 3 + k) % PIECES * PIECE, PIECE / 2, 1024);
+                    for (int k = 0; k < 2; ++k) {
+                        ok = wait(k == 0 ? &c.go[s] : &c.p_full[s], st & 1);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint64_t vd = sw128_desc(base + OFF_RING + (g + 3 + k) % PIECES * PIECE, PIECE / 2, 1024);
+                        if (elect_one()) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)  // 16 keys of 2 x 64 channels
                                 mma_f16_ts(d_o, d_s + k * 32 + i * 8, vd + ((i * 2048) >> 4), idesc_o, j > 0 || k + i > 0);
                             release(g + 3 + k, 1);  // before the scores: what a commit reports is all that came before it
+                            if (k == 1) {
+                                if (j + 1 < n) scores(g + PER_TILE, j + 2 == n);
+                                if (s == 0 ? j < n1 : j + 1 < n0) mbar_arrive(&c.go[s ^ 1]);  // the other side's turn
+                                if (j + 1 < n) release(g + PER_TILE, 3);
+                                else mma_commit(&c.o_full[s]);
+                            }
                         }
-                        if (!ok) break;
-                        if (j + 1 < n) scores(g + PER_TILE, j + 2 == n);
-                        if (s == 0 ? j < n1 : j + 1 < n0) mbar_arrive(&c.go[s ^ 1]);  // the other side's turn
-                        if (j + 1 < n) release(g + PER_TILE, 3);
-                        else mma_commit(&c.o_full[s]);
+                        __syncwarp();
                     }
-                    for (int j = n; j < most && ok; ++j, g += PER_TILE) {  // keys that only the other side sees
-                        const uint32_t t = jt + j;
-                        ok = wait.alone(&c.k_full[t & 1], (t >> 1) & 1);
-                        for (int k = 0; k < 3 && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
-                        ok = ok && wait.alone(&c.v_full[t & 1], (t >> 1) & 1);
-                        for (int k = 3; k < PER_TILE && ok; ++k) mbar_arrive(&c.empty[(g + k) % PIECES]);
-                    }
-                    if (!ok) break;
-                    jt += most;
                 }
-                if (!ok) {  // let issued products finish before the block ends
-                    mma_commit(&c.drain_bar[s]);
-                    drain(&c.drain_bar[s], 0);
+                for (int j = n; j < most && ok; ++j, g += PER_TILE) {  // keys that only the other side sees
+                    const uint32_t t = jt + j;
+                    ok = wait(&c.k_full[t & 1], (t >> 1) & 1);
+                    if (ok && lane < 3) mbar_arrive(&c.empty[(g + lane) % PIECES]);
+                    ok = ok && wait(&c.v_full[t & 1], (t >> 1) & 1);
+                    if (ok && lane < 2) mbar_arrive(&c.empty[(g + 3 + lane) % PIECES]);
+                    __syncwarp();
                 }
+                if (!ok) break;
+                jt += most;
             }
-            __syncwarp();
+            if (!ok) {  // let issued products finish before the block ends
+                if (elect_one()) mma_commit(&c.drain_bar[s]);
+                __syncwarp();
+                drain(&c.drain_bar[s], 0);
+            }
         } else {
             // ---------------------------------------------------------------- arrivals: tells the sides' steps of them
-            if (elect_one()) {
-                uint32_t it = 0, jt = 0, st[2] = {0, 0};
-                bool ok = true;
-                while (true) {
-                    ok = wait.alone(&c.item_full[it & 1], (it >> 1) & 1);
-                    if (!ok) break;
-                    const Item w = c.item[it & 1];
-                    mbar_arrive(&c.item_empty[it & 1]);
-                    ++it;
-                    if (!w.real) break;
-                    const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), most = max(n0, n1);
-                    for (int j = 0; j < most && ok; ++j, ++jt) {
-                        ok = wait.alone(&c.v_full[jt & 1], (jt >> 1) & 1);
+            uint32_t it = 0, jt = 0, st[2] = {0, 0};
+            bool ok = true;
+            while (true) {
+                ok = wait(&c.item_full[it & 1], (it >> 1) & 1);
+                if (!ok) break;
+                const Item w = c.item[it & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.item_empty[it & 1]);
+                ++it;
+                if (!w.real) break;
+                const int n0 = w.tiles(0, a.causal), n1 = w.tiles(1, a.causal), most = max(n0, n1);
+                for (int j = 0; j < most && ok; ++j, ++jt) {
+                    ok = wait(&c.v_full[jt & 1], (jt >> 1) & 1);
 #pragma unroll
-                        for (int s = 0; s < 2; ++s) {  // one step at a time, here and below
-                            if (j >= (s == 0 ? n0 : n1)) continue;
-                            ok = ok && (st[s] == 0 || wait.alone(&c.go[s], (st[s] - 1) & 1));
-                            if (ok) mbar_arrive(&c.go[s]);
-                        }
-                        if (j + 1 < most) ok = ok && wait.alone(&c.k_full[(jt + 1) & 1], ((jt + 1) >> 1) & 1);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            if (j >= (s == 0 ? n0 : n1)) continue;
-                            ok = ok && (st[s] == 0 || wait.alone(&c.p_full[s], (st[s] - 1) & 1));
-                            if (ok) mbar_arrive(&c.p_full[s]);
-                            ++st[s];
-                        }
+                    for (int s = 0; s < 2; ++s) {  // one step at a time, here and below
+                        if (j >= (s == 0 ? n0 : n1)) continue;
+                        ok = ok && (st[s] == 0 || wait(&c.go[s], (st[s] - 1) & 1));
+                        if (ok && lane == 0) mbar_arrive(&c.go[s]);
                     }
-                    if (!ok) break;
+                    if (j + 1 < most) ok = ok && wait(&c.k_full[(jt + 1) & 1], ((jt + 1) >> 1) & 1);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (j >= (s == 0 ? n0 : n1)) continue;
+                        ok = ok && (st[s] == 0 || wait(&c.p_full[s], (st[s] - 1) & 1));
+                        if (ok && lane == 0) mbar_arrive(&c.p_full[s]);
+                        ++st[s];
+                    }
                 }
+                if (!ok) break;
             }
-            __syncwarp();
         }
     }
     tc_fence_before_sync();

@@ -76,6 +76,17 @@ __device__ __forceinline__ void tmem_st16_nw(uint32_t taddr, const uint32_t (&v)
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+                 "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+                 "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                 : "memory");
+}
+
 // 16 lanes read twice, as tmem_ld16_x2, without waiting.
 template <int SPLIT>
 __device__ __forceinline__ void tmem_ld16_x2_nw(uint32_t taddr, uint32_t (&r)[16]) {
@@ -117,41 +128,37 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // The waits of a block whose warps have different roles.  A wait that gives up (after `polls` polls or 2 s) raises
 // KDA_DEVFLAG_TIMEOUT and the block's abort word, at which every other wait of the block gives up too, so that
-// all roles leave their loops, drain what they have in flight (drain(), default bound) and meet at the end.
+// all roles leave their loops, drain what they have in flight (drain(), default bound) and meet at the end.  Only the
+// first look is inlined: with some thirty waits in a kernel, the loops would be most of its code, and warps would stand
+// without instructions.
 struct RoleWait {
     uint32_t polls;
     volatile uint32_t* abort_word;  // shared memory
     unsigned int* flags;
 
-    __device__ __forceinline__ bool aborted() const { return *abort_word != 0u; }
-    __device__ __forceinline__ void give_up() const {
-        *abort_word = 1u;
-        raise_flag(flags, KDA_DEVFLAG_TIMEOUT);
-    }
-    // For one thread: what it waits for is done (the others of its warp learn of a failure from it).
-    __device__ __forceinline__ bool alone(uint64_t* bar, uint32_t parity) const {
-        WaitBudget budget;
-        for (uint32_t i = 0; i < polls; ++i) {
-            if (mbar_poll(bar, parity)) return true;
-            if (((i & 7u) == 7u && aborted()) || budget.expired()) break;
-        }
-        give_up();
-        return false;
-    }
-    // Called by whole warps; the answer is the same for all lanes.
-    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    __device__ __noinline__ static bool keep_looking(uint64_t* bar, uint32_t parity, uint32_t polls,
+                                                     volatile uint32_t* abort_word, unsigned int* flags) {
         WaitBudget budget;
         bool done = false;
-        for (uint32_t i = 0; i < polls; ++i) {
+        for (uint32_t i = 1; i < polls; ++i) {
             done = mbar_poll(bar, parity);
-            if (done || ((i & 7u) == 7u && aborted()) || budget.expired()) break;
+            if (done || ((i & 7u) == 7u && *abort_word != 0u) || budget.expired()) break;
         }
         done = __all_sync(0xffffffffu, done);
-        if (!done) give_up();
+        if (!done) {
+            *abort_word = 1u;
+            raise_flag(flags, KDA_DEVFLAG_TIMEOUT);
+        }
         return done;
     }
+    // For a converged warp, whose lanes all look and get the same answer.  (One lane that looks for all, the others waiting
+    // for it, took 35% longer in kda_mla_prefill.cu: the hardware suspends a whole warp at a barrier, not one lane.)
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        if (polls > 0 && __all_sync(0xffffffffu, mbar_poll(bar, parity))) return true;
+        return keep_looking(bar, parity, polls, abort_word, flags);
+    }
 };
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity, 1u << 26); }
+static __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity, 1u << 26); }
 
 // Byte offset of byte `col` of row `row` in a tile of 128-byte rows whose 16-byte chunks are permuted by XOR with
 // (row % 8): the 128-byte swizzle of TMA and of the matrix descriptors (tile base 1024-byte aligned).
