@@ -154,10 +154,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int s = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t at_s = tmem + lanes + COL_S + s * 128, at_o = tmem + lanes + COL_O + s * 128;
-        // the scale in log2 units, never 0: a hidden score, infinite of the other sign, gives a weight of 0
-        const bool negate = a.scale < 0.f;
-        const float sl2 = copysignf(fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f), negate ? -1.f : 1.f);
-        const uint32_t hidden = negate ? 0x7F800000u : 0xFF800000u;
+        // the scale in log2 units, never 0, so that a hidden score (-infinity) gives a weight of 0; where it is negative the
+        // products are formed with -Q
+        const float sl2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
         uint32_t it = 0, jt = 0, st = 0, outs = 0, ends = 0;
         bool ok = true;
         while (true) {
@@ -181,25 +180,25 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // The 128 scores in two passes of four quarters, each read from tensor memory while the one before is worked
                 // on; the loops stay loops, which keeps the code in the instruction caches (fully unrolled, with all
                 // scores in registers, warps stood without instructions a fifth of the time).
-                const bool edge = j * ROWS + ROWS - 1 > warp_see;  // some query of the warp does not see the whole tile
                 uint32_t xa[32], xb[32];
+                if (j * ROWS + ROWS - 1 > warp_see) {  // some query of the warp does not see the whole tile: hide scores
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const int left = see - j * ROWS - k * 32;  // the last column that this query sees
+                        tmem_ld32_nw(at_s + k * 32, xa);
+                        tmem_ld_wait();
+                        after_ld_wait(xa);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e > left) xa[e] = 0xFF800000u;
+                        tmem_st32_nw(at_s + k * 32, xa);
+                    }
+                    tmem_st_wait();
+                }
                 float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                const auto look = [&](uint32_t (&x)[32], int col) {
-                    if (edge) {  // hidden scores are written back as such for the second pass
-                        const int left = see - j * ROWS - col;  // the last column that this query sees
+                const auto look = [&](const uint32_t (&x)[32]) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (k > left) x[k] = hidden;
-                        tmem_st32_nw(at_s + col, x);
-                        tmem_st_wait();
-                    }
-                    if (negate) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], -__uint_as_float(x[k]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(x[k]));
-                    }
+                    for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(x[k]));
                 };
                 tmem_ld32_nw(at_s, xa);
                 tmem_ld_wait();
@@ -207,11 +206,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     tmem_ld32_nw(at_s + h * 64 + 32, xb);
-                    look(xa, h * 64);
+                    look(xa);
                     tmem_ld_wait();
                     after_ld_wait(xb);
                     tmem_ld32_nw(at_s + (h == 0 ? 64 : 0), xa);  // at last the second pass's first quarter
-                    look(xb, h * 64 + 32);
+                    look(xb);
                     tmem_ld_wait();
                     after_ld_wait(xa);
                 }
@@ -236,7 +235,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++ends;
                     if (!ok) break;
                 }
-                const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fabsf(sl2);
+                const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * sl2;
                 const bool move = top > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
                     float f = 1.f;
@@ -415,7 +414,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const uint32_t jt = g / PER_TILE;
                         row = w.k0 + j * ROWS;
                         uint64_t *kb = &c.k_full[jt & 1], *vb = &c.v_full[jt & 1];
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < PER_TILE; ++k) {
                             const uint32_t slot = g % PIECES;
                             // the second side is half a step behind: its queries come after the first keys
@@ -473,7 +472,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t d_s = tm + COL_S + s * 128, d_o = tm + COL_O + s * 128;
             const uint64_t q = sw128_desc(base + s * 3 * PIECE, 16, 1024);
-            constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false), idesc_o = idesc_bf16(128, 128, false, true);
+            constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
+            const uint32_t idesc_s = idesc_bf16(128, 128, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);  // negated A
             // Whole warps wait, one lane issues.
             const auto scores = [&](uint32_t g, bool last) {
 #pragma unroll
