@@ -54,14 +54,17 @@ struct Shape {
     static constexpr int NQ = E4M3 ? 2 * R : R;            // columns of the latent products (two parts for e4m3)
     static constexpr int BLOCKS = E4M3 ? 4 : 8;            // 128-byte column blocks of a latent row
     static constexpr int BLK = TOK * 128;                  // one block of a tile
-    static constexpr int STAGE = (BLOCKS + 1) * BLK;       // latents, then the positional keys
-    static constexpr int STAGES = E4M3 ? 4 : 2;
-    static constexpr int QBUFS = !E4M3 && R == 32 ? 2 : 1;
+    static constexpr int PIECE = 4 * BLK;                  // four blocks of latents: the ring's unit
+    static constexpr int NP = BLOCKS / 4;                  // pieces of a tile
+    static constexpr int PIECES = R == 32 ? 5 : 4;
+    static constexpr int PES = R == 32 ? 3 : 2;            // tiles of positional keys
+    static constexpr int SLOTS = (PIECES + NP - 1) / NP;   // tiles in flight, the one being freed included
     static constexpr int QBYTES = BLOCKS * NQ * 128 + R * 128;
     static constexpr int PROW = E4M3 ? NQ : NQ * 2;        // weights: one row of all columns per token, 64 or 128 bytes
     static constexpr int PBYTES = TOK * PROW;
-    static constexpr int OFF_Q = STAGES * STAGE;
-    static constexpr int OFF_P = OFF_Q + QBUFS * QBYTES;
+    static constexpr int OFF_PE = PIECES * PIECE;
+    static constexpr int OFF_Q = OFF_PE + PES * BLK;
+    static constexpr int OFF_P = OFF_Q + QBYTES;
     static constexpr int OFF_CTL = OFF_P + PBYTES;
     // tensor memory columns
     static constexpr int S_COLS = E4M3 ? NQ + R : R;       // one score buffer: latent part(s), positional part
@@ -72,14 +75,14 @@ struct Shape {
 
 template <int R, bool E4M3>
 struct Ctl {
-    uint64_t kv_full[4], kv_empty[4], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full, pv_done, drain_bar[2];
+    uint64_t kv_full[5], kv_empty[5], pe_empty[3], q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain_bar[2];
     uint32_t tmem;
     uint32_t abort_word;
-    uint32_t bad[4];          // per stage: page slots of the tile with a bad page number
+    uint32_t bad[5];          // per tile in flight: page slots of the tile with a bad page number
     long long scan[THREADS / 32];  // partial sums of the start search
     int b0, t0;
     long long first, end, left, total;  // the range of this CTA, the tiles of it from t0 on (and later leads), all
-    alignas(16) float scale[E4M3 ? 4 : 1][TOK];  // e4m3: the tokens' scales, per stage
+    alignas(16) float scale[E4M3 ? Shape<R, E4M3>::SLOTS : 1][TOK];  // e4m3: the tokens' scales, per tile in flight
     alignas(16) float qscale[E4M3 ? R : 4];      // e4m3: the query rows' scales
     alignas(16) float red[4][R];          // per warp and row: maxima; at a segment's end sums
     alignas(16) float factor[R];                 // per row: rescaling factor; at a segment's end 1 / l
@@ -224,13 +227,14 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (tid == 0) {
             c.abort_word = 0u;
             c.left = 0;
-            for (int i = 0; i < SH::STAGES; ++i) {
-                mbar_init(&c.kv_full[i], 1);
+            for (int i = 0; i < 5; ++i) {
+                mbar_init(&c.kv_full[i], SH::NP);
                 mbar_init(&c.kv_empty[i], 1);
             }
+            for (int i = 0; i < 3; ++i) mbar_init(&c.pe_empty[i], 1);
+            mbar_init(&c.q_full, E4M3 ? 8 : 1);
+            mbar_init(&c.q_empty, 1);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&c.q_full[i], E4M3 ? 8 : 1);
-                mbar_init(&c.q_empty[i], 1);
                 mbar_init(&c.s_full[i], 1);
                 mbar_init(&c.s_empty[i], 8);
             }
@@ -299,81 +303,85 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
         if (warp == 8) {
             // ---------------------------------------------------------------- loads
-            // A tile's copies: per page slot of up to 64 tokens the latent blocks (one box where a page holds the whole
-            // tile), the positional keys and the scales.  The page table is read 32 entries at a time, one such piece
-            // ahead.
+            // A tile's copies: per page slot of up to 64 tokens the latent blocks (one box of four where a page holds the
+            // whole tile), the positional keys and the scales, each as soon as its place in the ring is free.  A tile's
+            // page numbers are read, by all lanes alike, a tile ahead.  (One lane per slot and shuffles: 1,500 cycles a
+            // tile, as shuffles queue behind the other warps' shared-memory traffic; that bound the e4m3 form.)
             const int shift = min(a.cache.page_shift, 6), prow = 1 << shift, slots = TOK >> shift;
-            uint32_t g = 0, seg = 0, queries = 0;  // tiles and query tiles issued
+            uint32_t g = 0, n = 0;  // tiles and pieces issued
             bool ok = true;
             do {
                 const int32_t* table = a.cache.page_table + static_cast<int64_t>(w.b) * a.cache.max_pages;
-                const int entries = (w.len + a.cache.page_size - 1) >> a.cache.page_shift;
-                const auto piece = [&](int k) { return k * 32 + lane < entries ? table[k * 32 + lane] : 0; };
-                int k = (w.t * TOK) >> a.cache.page_shift >> 5;
-                int now = piece(k), later = piece(k + 1);
-                if (!E4M3) {  // the segment's queries
-                    const uint32_t qb = seg % SH::QBUFS, qn = seg / SH::QBUFS;
-                    ok = wait(&c.q_empty[qb], (qn & 1) ^ 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        unsigned char* q = smem + SH::OFF_Q + qb * SH::QBYTES;
-                        mbar_arrive_expect_tx(&c.q_full[qb], SH::QBYTES);
-                        tma_load_4d(q, &tm_q, 0, row0, 0, w.b, &c.q_full[qb]);
-                        tma_load_4d(q + SH::BLOCKS * SH::NQ * 128, &tm_qp, 0, row0, 0, w.b, &c.q_full[qb]);
-                    }
-                    ++queries;
-                    __syncwarp();
-                }
-                for (int i = 0; i < w.n; ++i, ++g) {
-                    const uint32_t st = g % SH::STAGES;
-                    const int pos = (w.t + i) * TOK, entry = pos >> a.cache.page_shift;
-                    if (entry >> 5 != k) {
-                        ++k;
-                        now = later;
-                        later = piece(k + 1);
-                    }
-                    const int mine = __shfl_sync(0xffffffffu, now, (entry + lane) & 31);  // slot `lane`
-                    const bool real = lane < slots && pos + lane * prow < w.len;
-                    const bool bad = real && (mine < 0 || mine >= a.cache.num_pages);
-                    if (bad) raise_flag(a.flags, KDA_DEVFLAG_PAGE_TABLE);
-                    const uint32_t bads = __ballot_sync(0xffffffffu, bad), used = __ballot_sync(0xffffffffu, real && !bad);
-                    ok = wait(&c.kv_empty[st], ((g / SH::STAGES) & 1) ^ 1);
-                    if (!ok) break;
-                    unsigned char* kv = smem + st * SH::STAGE;
-                    int row[4];  // pool row of each slot's first token
+                const auto fetch = [&](int (&page)[4], int i) {
+                    const int pos = (w.t + i) * TOK;
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        row[x] = static_cast<int>((static_cast<int64_t>(__shfl_sync(0xffffffffu, mine, x)) << a.cache.page_shift) +
+                        page[x] = x < slots && i < w.n && pos + x * prow < w.len ? __ldg(table + ((pos + x * prow) >> a.cache.page_shift))
+                                                                                 : 0;
+                };
+                int page[4];
+                fetch(page, 0);
+                for (int i = 0; i < w.n; ++i, ++g) {
+                    const uint32_t slot = g % SH::SLOTS;
+                    const int pos = (w.t + i) * TOK;
+                    uint32_t bads = 0u, used = 0u;
+                    int row[4];  // pool row of each slot's first token
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const bool real = x < slots && pos + x * prow < w.len;
+                        const bool good = page[x] >= 0 && page[x] < a.cache.num_pages;
+                        bads |= real && !good ? 1u << x : 0u;
+                        used |= real && good ? 1u << x : 0u;
+                        row[x] = static_cast<int>((static_cast<uint32_t>(page[x]) << a.cache.page_shift) +
                                                   ((pos + x * prow) & (a.cache.page_size - 1)));
-                    if (elect_one()) {
-                        c.bad[st] = bads;
-                        mbar_arrive_expect_tx(&c.kv_full[st], static_cast<uint32_t>(__popc(used)) * prow *
-                                                                  ((SH::BLOCKS + 1) * 128 + (E4M3 ? 4 : 0)));
+                    }
+                    if (bads) raise_flag(a.flags, KDA_DEVFLAG_PAGE_TABLE);
+                    fetch(page, i + 1);
+                    const uint32_t tokens = static_cast<uint32_t>(__popc(used)) * prow, at_pe = g % SH::PES;
+                    int done = 0;  // arrivals for the tile
+                    for (; done < SH::NP; ++done, ++n) {
+                        const uint32_t at = n % SH::PIECES, turn = ((n / SH::PIECES) & 1) ^ 1;
+                        ok = done == 0 ? wait.both(&c.kv_empty[at], turn, &c.pe_empty[at_pe], ((g / SH::PES) & 1) ^ 1)
+                                       : wait(&c.kv_empty[at], turn);
+                        if (!ok) break;
+                        unsigned char* kv = smem + at * SH::PIECE;
+                        if (elect_one()) {
+                            if (done == 0) c.bad[slot] = bads;
+                            mbar_arrive_expect_tx(&c.kv_full[slot], tokens * (512 + (done == 0 ? 128 + (E4M3 ? 4 : 0) : 0)));
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            if (used >> x & 1u) {
-                                unsigned char* dst = kv + x * prow * 128;
-                                if (prow == TOK) {
-                                    tma_load_3d(dst, &tm_kv, 0, row[x], 0, &c.kv_full[st]);
-                                } else {
+                            for (int x = 0; x < 4; ++x) {
+                                if (used >> x & 1u) {
+                                    unsigned char* dst = kv + x * prow * 128;
+                                    if (prow == TOK) {
+                                        tma_load_3d(dst, &tm_kv, 0, row[x], done * 4, &c.kv_full[slot]);
+                                    } else {
 #pragma unroll
-                                    for (int n = 0; n < SH::BLOCKS; ++n)
-                                        tma_load_3d(dst + n * SH::BLK, &tm_kv, 0, row[x], n, &c.kv_full[st]);
+                                        for (int k = 0; k < 4; ++k)
+                                            tma_load_3d(dst + k * SH::BLK, &tm_kv, 0, row[x], done * 4 + k, &c.kv_full[slot]);
+                                    }
+                                    if (done == 0) {
+                                        tma_load_3d(smem + SH::OFF_PE + at_pe * SH::BLK + x * prow * 128, &tm_pe, 0, row[x], 0,
+                                                    &c.kv_full[slot]);
+                                        if (E4M3)
+                                            bulk_load(&c.scale[slot][x * prow], a.cache.scale + row[x], prow * 4, &c.kv_full[slot]);
+                                    }
                                 }
-                                tma_load_3d(dst + SH::BLOCKS * SH::BLK, &tm_pe, 0, row[x], 0, &c.kv_full[st]);
-                                if (E4M3) bulk_load(&c.scale[st][x * prow], a.cache.scale + row[x], prow * 4, &c.kv_full[st]);
                             }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) {  // the rest of the tile stays empty
+                        if (lane == 0)
+                            for (; done < SH::NP; ++done) mbar_arrive(&c.kv_full[slot]);
+                        __syncwarp();
+                        ++g;
+                        break;
+                    }
                 }
-                ++seg;
             } while (ok && w.next(a));
             if (!ok) {  // let what is in flight land before the block ends
-                for (uint32_t i = g > SH::STAGES ? g - SH::STAGES : 0; i < g; ++i)
-                    drain(&c.kv_full[i % SH::STAGES], (i / SH::STAGES) & 1);
-                for (uint32_t i = queries > SH::QBUFS ? queries - SH::QBUFS : 0; i < queries; ++i)
-                    drain(&c.q_full[i % SH::QBUFS], (i / SH::QBUFS) & 1);
+                for (uint32_t i = g > SH::SLOTS ? g - SH::SLOTS : 0; i < g; ++i)
+                    drain(&c.kv_full[i % SH::SLOTS], (i / SH::SLOTS) & 1);
             }
         } else if (warp == 9) {
             // ---------------------------------------------------------------- first products: scores
@@ -384,32 +392,45 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             uint32_t g = 0, seg = 0;
             bool ok = true;
             do {
-                const uint32_t qb = seg % SH::QBUFS;
-                ok = wait(&c.q_full[qb], (seg / SH::QBUFS) & 1);
+                if (!E4M3) {  // the segment's queries, once the last one's scores are done
+                    ok = wait(&c.q_empty, (seg & 1) ^ 1);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&c.q_full, SH::QBYTES);
+                        tma_load_4d(smem + SH::OFF_Q, &tm_q, 0, row0, 0, w.b, &c.q_full);
+                        tma_load_4d(smem + SH::OFF_Q + SH::BLOCKS * SH::NQ * 128, &tm_qp, 0, row0, 0, w.b, &c.q_full);
+                    }
+                    __syncwarp();
+                }
+                ok = wait(&c.q_full, seg & 1);
+                if (!E4M3 && !ok) drain(&c.q_full, seg & 1);
                 for (int i = 0; i < w.n && ok; ++i) {
-                    const uint32_t st = g % SH::STAGES;
-                    ok = wait(&c.s_empty[g & 1], ((g >> 1) & 1) ^ 1) && wait(&c.kv_full[st], (g / SH::STAGES) & 1);
+                    ok = wait.both(&c.s_empty[g & 1], ((g >> 1) & 1) ^ 1, &c.kv_full[g % SH::SLOTS], (g / SH::SLOTS) & 1);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t d = tm + (g & 1) * SH::S_COLS;
-                    const uint64_t k0 = sw128_desc(base + st * SH::STAGE, 16, 1024);
-                    const uint64_t q0 = sw128_desc(qs + qb * SH::QBYTES, 16, 1024);
+                    const uint64_t q0 = sw128_desc(qs, 16, 1024), p0 = sw128_desc(base + SH::OFF_PE + g % SH::PES * SH::BLK, 16, 1024);
+                    uint64_t k0[SH::NP];
+#pragma unroll
+                    for (int h = 0; h < SH::NP; ++h)
+                        k0[h] = sw128_desc(base + (g * SH::NP + h) % SH::PIECES * SH::PIECE, 16, 1024);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < SH::BLOCKS; ++k)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint64_t da = k0 + ((k * SH::BLK + j * 32) >> 4);
+                                const uint64_t da = k0[k / 4] + ((k % 4 * SH::BLK + j * 32) >> 4);
                                 const uint64_t db = q0 + ((k * SH::NQ * 128 + j * 32) >> 4);
                                 if (E4M3) mma_f8(d, da, db, idesc_s, k + j > 0);
                                 else mma_f16(d, da, db, idesc_s, k + j > 0);
                             }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma_f16(E4M3 ? d + SH::NQ : d, k0 + ((SH::BLOCKS * SH::BLK + j * 32) >> 4),
+                            mma_f16(E4M3 ? d + SH::NQ : d, p0 + ((j * 32) >> 4),
                                     q0 + ((SH::BLOCKS * SH::NQ * 128 + j * 32) >> 4), idesc_p, E4M3 ? j > 0 : 1);
                         mma_commit(&c.s_full[g & 1]);
-                        if (i + 1 == w.n) mma_commit(&c.q_empty[qb]);
+                        mma_commit(&c.pe_empty[g % SH::PES]);
+                        if (!E4M3 && i + 1 == w.n) mma_commit(&c.q_empty);
                     }
                     __syncwarp();
                     ++g;
@@ -434,21 +455,27 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     ok = wait(&c.p_full, g & 1);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t st = g % SH::STAGES;
-                    const uint64_t v0 = sw128_desc(base + st * SH::STAGE, SH::BLK, 1024);
+                    uint32_t at[SH::NP];
+                    uint64_t v0[SH::NP];
+#pragma unroll
+                    for (int h = 0; h < SH::NP; ++h) {
+                        at[h] = (g * SH::NP + h) % SH::PIECES;
+                        v0[h] = sw128_desc(base + at[h] * SH::PIECE, SH::BLK, 1024);
+                    }
                     if (elect_one()) {
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
+                        for (int ch = 0; ch < 4; ++ch) {
 #pragma unroll
                             for (int k = 0; k < (E4M3 ? 2 : 4); ++k) {
                                 const uint32_t d = tm + SH::COL_O + ch * SH::NQ;
                                 const uint64_t pk = ps + ((k * (E4M3 ? 32 : 16) * SH::PROW) >> 4);
                                 if (E4M3)  // 32 tokens of 128 channels: four groups of 8 tokens, 1024 bytes each
-                                    mma_f8(d, v0 + ((ch * SH::BLK + k * 4096) >> 4), pk, idesc_o, i > 0 || k > 0);
+                                    mma_f8(d, v0[0] + ((ch * SH::BLK + k * 4096) >> 4), pk, idesc_o, i > 0 || k > 0);
                                 else       // 16 tokens of 2 x 64 channels
-                                    mma_f16(d, v0 + ((2 * ch * SH::BLK + k * 2048) >> 4), pk, idesc_o, i > 0 || k > 0);
+                                    mma_f16(d, v0[ch / (4 / SH::NP)] + ((ch % 2 * 2 * SH::BLK + k * 2048) >> 4), pk, idesc_o, i > 0 || k > 0);
                             }
-                        mma_commit(&c.kv_empty[st]);
+                            if (ch % (4 / SH::NP) == 4 / SH::NP - 1) mma_commit(&c.kv_empty[at[ch / (4 / SH::NP)]]);
+                        }
                         mma_commit(&c.pv_done);
                     }
                     __syncwarp();
@@ -528,7 +555,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 *reinterpret_cast<uint4*>(q + SH::BLOCKS * SH::NQ * 128 + sw128_byte(r, part * 16)) = pe;
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c.q_full[0]);
+                if (lane == 0) mbar_arrive(&c.q_full);
             };
             if (E4M3) {
                 load_queries(w.b);
@@ -544,14 +571,14 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         static_cast<const __nv_bfloat16*>(a.q_latent) +
                         (static_cast<int64_t>(w.b + 1) * rows + row0 + (tid >> 3)) * kMlaLatent + (tid & 7) * 64));
                 for (int t = 0; t < w.n; ++t, ++g) {
-                    const uint32_t st = g % SH::STAGES;
-                    ok = ok && wait(&c.kv_full[st], (g / SH::STAGES) & 1) && wait(&c.s_full[g & 1], (g >> 1) & 1);
+                    const uint32_t slot = g % SH::SLOTS;
+                    ok = ok && wait.both(&c.kv_full[slot], (g / SH::SLOTS) & 1, &c.s_full[g & 1], (g >> 1) & 1);
                     tc_fence_after_sync();
                     float x[HH];
                     const uint32_t s_at = tmem + lane_base + (g & 1) * SH::S_COLS + wg * (R / 2);
                     float ts = 1.f, ls = 0.f;   // the token's scale and its log2
                     const int pos = (w.t + t) * TOK + tok;
-                    const uint32_t bads = c.bad[st];
+                    const uint32_t bads = c.bad[slot];
                     const bool seen = pos < w.len && !(bads >> (tok >> min(a.cache.page_shift, 6)) & 1u);
                     if constexpr (E4M3) {
                         uint32_t hi[HH], lo[HH], pe[HH];
@@ -559,7 +586,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         tmem_ld8_x2_nw<HH>(s_at + R, lo);
                         tmem_ld8_x2_nw<HH>(s_at + SH::NQ, pe);
                         if (seen) {
-                            ts = c.scale[st][tok];
+                            ts = c.scale[slot][tok];
                             ls = __log2f(ts);
                         }
                         tmem_ld_wait();
@@ -603,11 +630,12 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         // weight of 0 meets no NaN in the second product (the first one is done with them)
                         if (!seen && half == 0) {
 #pragma unroll 1
-                            for (int k = wg; k < SH::BLOCKS; k += 2)
+                            for (int k = wg; k < SH::BLOCKS; k += 2) {
+                                unsigned char* blk = smem + (g * SH::NP + k / 4) % SH::PIECES * SH::PIECE + k % 4 * SH::BLK;
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    *reinterpret_cast<uint4*>(smem + st * SH::STAGE + k * SH::BLK + tok * 128 + j * 16) =
-                                        make_uint4(0, 0, 0, 0);
+                                for (int j = 0; j < 8; ++j)  // neighbouring tokens' stores in different banks
+                                    *reinterpret_cast<uint4*>(blk + tok * 128 + ((j + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
                         }
                     }
                     // Does some score exceed its row's reference by too much?  Seldom; only then are the tile's maxima
@@ -709,8 +737,6 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&c.p_full);
                 }
-                if (stop) break;
-
                 if (stop) break;
 
                 // ---- the segment's end: sums over its tokens, then the output from tensor memory
@@ -974,7 +1000,7 @@ cudaError_t launch(const MlaDecodeArgs& a, const Grid& g) {
     const void* latent = none ? a.q_latent : a.cache.latent;
     const void* cpe = none ? a.q_pe : a.cache.pe;
     if (!encode_q(&q, a.q_latent, kMlaLatent, rows, a.B, R) || !encode_q(&qp, a.q_pe, kMlaPe, rows, a.B, R) ||
-        !encode_pool(&kv, latent, E4M3 ? 1 : 2, pool, SH::BLOCKS, box, box == TOK ? SH::BLOCKS : 1) ||
+        !encode_pool(&kv, latent, E4M3 ? 1 : 2, pool, SH::BLOCKS, box, box == TOK ? 4 : 1) ||
         !encode_pool(&pe, cpe, 2, pool, 1, box, 1))
         return cudaErrorInvalidValue;
     const int ctas = g.groups * g.row_tiles;

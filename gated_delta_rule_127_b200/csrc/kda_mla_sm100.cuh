@@ -157,6 +157,15 @@ struct RoleWait {
         if (polls > 0 && __all_sync(0xffffffffu, mbar_poll(bar, parity))) return true;
         return keep_looking(bar, parity, polls, abort_word, flags);
     }
+    // Two barriers, looked at together: a look takes some 250 cycles beside busy warps.
+    __device__ __forceinline__ bool both(uint64_t* one, uint32_t one_parity, uint64_t* two, uint32_t two_parity) const {
+        if (polls > 0) {
+            const bool first = mbar_poll(one, one_parity), second = mbar_poll(two, two_parity);
+            if (__all_sync(0xffffffffu, first && second)) return true;
+        }
+        return keep_looking(one, one_parity, polls, abort_word, flags) &&
+               keep_looking(two, two_parity, polls, abort_word, flags);
+    }
 };
 static __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity, 1u << 26); }
 
