@@ -139,6 +139,7 @@ constexpr int64_t kManyRows = 148 * 32 * ROWS;
 template <typename T, bool E4M3, int N>
 __global__ void __launch_bounds__(WARPS * 32) mla_cache_write_kernel(const __grid_constant__ MlaCacheCopyArgs a) {
     using C = std::conditional_t<E4M3, uint8_t, __nv_bfloat16>;
+    mla::after_previous();
     if (blockIdx.x == 0) mla::check_cu(a.cu_seqlens, a.T, a.B, a.flags);
     const int lane = threadIdx.x & 31;
     const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N;
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(WARPS * 32) mla_cache_write_kernel(const __gri
 template <typename T, bool E4M3, int N>
 __global__ void __launch_bounds__(WARPS * 32) mla_cache_read_kernel(const __grid_constant__ MlaCacheCopyArgs a) {
     using C = std::conditional_t<E4M3, uint8_t, __nv_bfloat16>;
+    mla::after_previous();
     if (blockIdx.x == 0) mla::check_cu(a.cu_seqlens, a.T, a.B, a.flags);
     const int lane = threadIdx.x & 31;
     const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N;
@@ -224,14 +226,9 @@ cudaError_t launch(const MlaCacheCopyArgs& a) {
     const bool many = a.T >= kManyRows;
     const int64_t per = WARPS * (many ? ROWS : 1);
     const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per)), block(WARPS * 32);
-    if (WRITE) {
-        if (many) mla_cache_write_kernel<T, E4M3, ROWS><<<grid, block, 0, a.stream>>>(a);
-        else mla_cache_write_kernel<T, E4M3, 1><<<grid, block, 0, a.stream>>>(a);
-    } else {
-        if (many) mla_cache_read_kernel<T, E4M3, ROWS><<<grid, block, 0, a.stream>>>(a);
-        else mla_cache_read_kernel<T, E4M3, 1><<<grid, block, 0, a.stream>>>(a);
-    }
-    return cudaGetLastError();
+    constexpr auto one = WRITE ? mla_cache_write_kernel<T, E4M3, 1> : mla_cache_read_kernel<T, E4M3, 1>;
+    constexpr auto several = WRITE ? mla_cache_write_kernel<T, E4M3, ROWS> : mla_cache_read_kernel<T, E4M3, ROWS>;
+    return launch_early(many ? several : one, grid, block, 0, a.stream, a);
 }
 
 template <bool WRITE>

@@ -11,6 +11,10 @@
 namespace kda {
 namespace mla {
 
+// Waits until the kernels before this one in the stream have ended and their writes are visible.  Every thread of a
+// kernel started by launch_early() calls it before its first access to memory that is not its own.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // First row and row count of sequence b of a packed batch of T rows (cu = NULL: equal lengths).  A bad
 // entry raises the flag and gives no rows.
 __device__ __forceinline__ int seq_rows(const int32_t* cu, int64_t T, int B, int b, int64_t& first,

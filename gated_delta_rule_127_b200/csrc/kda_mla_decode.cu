@@ -213,17 +213,6 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // ---- the range of this CTA: every thread sums its share of the sequences, then the one that holds the range's
     // first place finds its sequence
     {
-        const int per = (a.B + THREADS - 1) / THREADS, lo = min(tid * per, a.B), hi = min(lo + per, a.B);
-        const auto places = [&](int b) { return tiles_of(cached_len(a, b)) + SH::LEAD; };
-        long long mine = 0;
-        for (int b = lo; b < hi; ++b) mine += places(b);
-        long long upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += v;
-        }
-        if (lane == 31) c.scan[warp] = upto;
         if (tid == 0) {
             c.abort_word = 0u;
             c.left = 0;
@@ -246,6 +235,18 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         if (warp == 9) tmem_alloc(&c.tmem, 512);
         if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_kv : lane == 1 ? &tm_pe : lane == 2 ? &tm_q : &tm_qp);
+        mla::after_previous();
+        const int per = (a.B + THREADS - 1) / THREADS, lo = min(tid * per, a.B), hi = min(lo + per, a.B);
+        const auto places = [&](int b) { return tiles_of(cached_len(a, b)) + SH::LEAD; };
+        long long mine = 0;
+        for (int b = lo; b < hi; ++b) mine += places(b);
+        long long upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        if (lane == 31) c.scan[warp] = upto;
         __syncthreads();
         long long total = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
@@ -855,7 +856,7 @@ __global__ void __launch_bounds__(COMBINE) mla_combine_kernel(const __grid_const
                                                               int ctas) {
     static_assert(GROUPS <= COMBINE, "a thread per part");
     constexpr int WARPS = COMBINE / 32, AHEAD = 4;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    mla::after_previous();
     const Part p = part_of(a.workspace, ctas, R);
     const int4 meta = p.meta[blockIdx.x * 2 + blockIdx.z];  // sequence, first and last group
     if (meta.x < 0) return;
@@ -1004,19 +1005,10 @@ cudaError_t launch(const MlaDecodeArgs& a, const Grid& g) {
         !encode_pool(&pe, cpe, 2, pool, 1, box, 1))
         return cudaErrorInvalidValue;
     const int ctas = g.groups * g.row_tiles;
-    kernel<<<ctas, THREADS, smem, a.stream>>>(q, qp, kv, pe, a, g.row_tiles, g.groups);
-    err = cudaGetLastError();
+    err = launch_early(kernel, dim3(ctas), dim3(THREADS), smem, a.stream, q, qp, kv, pe, a, g.row_tiles, g.groups);
     if (err != cudaSuccess || !a.workspace) return err;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, kMlaLatent / 128, 2);
-    cfg.blockDim = dim3(COMBINE);
-    cfg.stream = a.stream;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_combine_kernel<R, TO>, a, g.row_tiles, ctas);
+    return launch_early(mla_combine_kernel<R, TO>, dim3(ctas, kMlaLatent / 128, 2), dim3(COMBINE), 0, a.stream, a,
+                        g.row_tiles, ctas);
 }
 
 template <typename TO>

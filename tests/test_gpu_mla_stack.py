@@ -92,3 +92,74 @@ def test_prefill_then_decode(dtype):
         y = gen.make_decode_step(step, B, H, 128, 128, seed=0, device=DEV)
         kda.kda_decode_step(y.q, y.k, y.v, y.log_alpha, y.beta, state)
     assert kda.kda_get_device_status() == (kda.KDA_OK, 0)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("last", ["kernel", "copy", "set", "join"])
+def test_calls_wait_for_what_comes_before(last, captured):
+    # write, read and decode may start while the work before them ends; its results are theirs all the same.  The slow
+    # work ends in the new tokens, the lengths and the queries; what comes last before the calls is a kernel, a copy, a
+    # memory set or another stream's event.
+    n, H = 40, 32
+    cache = Cache([n] * 8, 64, BF16, DEV).fill(3)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)  # noqa: E731
+    new = [(r(8, LATENT), r(8, PE), r(8, 1, H, LATENT), r(8, 1, H, PE)) for _ in range(3)]
+    lens = torch.full((8,), n, dtype=torch.int32, device=DEV)
+    cu = cu_of([1] * 8, DEV)
+    starts = lens - 1
+    now = [torch.zeros_like(t) for t in new[0]]
+    source = [torch.zeros_like(t) for t in new[0]]
+    out = [torch.zeros(8, 1, H, LATENT, dtype=BF16, device=DEV), torch.zeros(8, LATENT, dtype=BF16, device=DEV)]
+    big, spare = torch.randn(2048, 2048, generator=g, device=DEV), torch.ones(1 << 20, device=DEV)
+    lat, pe = torch.zeros(8, LATENT, dtype=BF16, device=DEV), torch.zeros(8, PE, dtype=BF16, device=DEV)
+    ws = torch.empty(kda.kda_mla_decode_workspace_size(8, 1, H), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+
+    def work():
+        def slow():
+            x = big
+            for _ in range(8):
+                x = (x @ big) * 0.02
+            zero = x[0, 0] * 0.0
+            for t, s in zip(now, source):
+                t.copy_(s + zero.to(BF16))
+        if last == "join":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                slow()
+            spare.add_(1)
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            slow()
+            if last == "copy":
+                now[2].copy_(source[2])
+            elif last == "set":
+                spare.zero_()
+        kda.kda_mla_cache_write(now[0], now[1], cache.latent, cache.pe, cache.table, lens, cu)
+        kda.kda_mla_cache_read(cache.latent, cache.pe, cache.table, cu, 8, starts=starts, latent=lat, pe=pe)
+        out[1].copy_(lat)
+        kda.kda_mla_decode(now[2], now[3], cache.latent, cache.pe, cache.table, lens, softmax_scale=SCALE, o=out[0],
+                           workspace=ws)
+
+    def set_inputs(i):
+        for s, t in zip(source, new[i]):
+            s.copy_(t)
+
+    set_inputs(0)
+    work()
+    torch.cuda.synchronize()
+    run = work
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            work()
+        run = graph.replay
+    for i in (1, 2, 0, 1):
+        set_inputs(i)
+        run()
+        got = out[0].clone()
+        torch.cuda.synchronize()
+        assert torch.equal(out[1], new[i][0]) and torch.equal(pe, new[i][1])
+        want, tol, _, _ = mla_ref.decode(new[i][2], new[i][3], cache, SCALE, BF16)
+        mla_ref.check(got, want, tol, "o")
