@@ -10,7 +10,7 @@
 // 32 or 64, the N side) still fill the tensor core's M, and the one shared-memory copy of C serves both: as the
 // K-major A operand first and as the MN-major A operand (C^T) second.  Each cached byte is read once from
 // memory; per tile of 72 KB (bf16) an SM's tensor core needs about 1,100 cycles for R = 32, its share of the
-// memory bandwidth about 3,100.
+// memory bandwidth about 3,000: memory is the bound, and the rings keep as much of it in flight as shared memory holds.
 //
 // e4m3: the codes are multiplied as they are (kind::f8f6f4).  Queries and weights enter as two e4m3 parts,
 // hi = e4m3(x) and lo = e4m3(16 (x - hi)), as 2 R columns of one product whose halves are added (hi + lo / 16) in
@@ -23,7 +23,7 @@
 //
 // Work split: all tiles of all sequences, in order, are cut into G equal ranges, one per CTA (per row tile), with a
 // few tiles' worth added before each sequence for what it costs to begin and end one (queries, first maxima, output:
-// about 8,000 cycles against 2,000 per e4m3 tile, 6,000 against 3,300 per bf16 tile; without it the CTAs with
+// about 8,000 cycles against 1,800 per e4m3 tile, 6,000 against 3,200 per bf16 tile; without it the CTAs with
 // the most sequences finished 20% after the median of a batch of 128).  A sequence that a cut falls into leaves
 // partial (m, l, O) in the workspace, which mla_combine_kernel joins in a fixed order.  The cuts are found on the device from seq_lens, so a captured call follows new lengths.
 //

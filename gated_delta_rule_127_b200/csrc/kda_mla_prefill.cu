@@ -20,15 +20,19 @@
 //
 // A thread per side issues its products, in turns: O += W V of a tile and the scores of the next one, then the other
 // thread the same for its side.  Without turns the sides' products mix on the tensor core, both sides' scores come
-// late and together, and the sides fall into step (6,180 cycles a tile).  A look at a barrier costs 250 cycles while the
-// softmax warps keep the special-function units' queue full, and the tensor core idles meanwhile; so a step looks at two:
-// `go` for half of its weights, this tile's values and the other side's turn, `p_full` for the other half and the next
-// tile's keys.  A warp of its own reports the loads there (4,100 cycles with a look at each barrier).
+// late and together, and the sides fall into step (2 to 25% slower, most over long keys).  A look at a barrier costs 250
+// cycles while the softmax warps keep the special-function units' queue full, and the tensor core idles meanwhile; so a
+// step looks at two: `go` for half of its weights, this tile's values and the other side's turn, `p_full` for the other
+// half and the next tile's keys.  A warp of its own reports the loads there.
 //
 // A CTA takes one item, 256 queries of a head, after another: the loads of the next one begin while the last tiles of
 // this one are computed, and its first scores while this one's output is written (about 14,000 cycles of an item that
 // would stand alone).  The grid has a block for every item; a running CTA takes over blocks that have not begun yet
-// (cluster launch control), so the hardware's order and balance stay.
+// (cluster launch control), which balances them; the blocks' order puts the large items first.
+//
+// Bound by the tensor core and the power that it draws.  Measured, causal, 32 heads: 8,192 tokens 585 us (1,170 TFLOP/s,
+// 71% of what a library's matrix product reaches in a burst, 84% of what it sustains), eight prompts of 63 to 2,500
+// tokens 305 us, 2,048 queries over up to 32,048 keys 1,144 us (1,140 TFLOP/s); a box that throttles adds up to a tenth.
 //
 // Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 finds the items and loads (TMA), 9 and 10 issue the
 // sides' products, 11 reports the loads' arrival.
@@ -45,10 +49,15 @@ using namespace sm100;
 
 constexpr int ROWS = 128;              // queries per side, keys per tile
 constexpr int THREADS = 384;
+// Steps in which the work is ordered by size.  1, one head after another: 672 us for 8,192 tokens, 308 for the eight
+// prompts, 1,104 for the long keys; 4: 585, 305, 1,144; 16: the eight prompts 340, as heads' keys and values are shared less.
+constexpr int LEVELS = 4;
 constexpr int PIECE = 16384, PIECES = 8, PER_TILE = 5;
 constexpr int OFF_RING = 2 * 3 * PIECE;                   // after both sides' queries (three blocks of 64 channels each)
 constexpr int OFF_CTL = OFF_RING + PIECES * PIECE;
 constexpr uint32_t COL_S = 0, COL_O = 256;                // tensor memory: per side 128 columns of each
+
+__device__ __forceinline__ int pairs_of(int queries) { return queries / (2 * ROWS) + (queries % (2 * ROWS) > 0); }
 
 struct Item {                          // 256 queries of a head
     int real;                          // 0: there are no more
@@ -137,7 +146,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     if (warp == 9) tmem_alloc(&c.tmem, 512);
     if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &tm_q : lane == 1 ? &tm_k : lane == 2 ? &tm_v : &tm_pe);
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (blockIdx.x == 0) {
         mla::check_cu(a.cu_q, a.Tq, a.B, a.flags);
         mla::check_cu(a.cu_k, a.Tk, a.B, a.flags);
     }
@@ -337,44 +346,70 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (warp == 8) {
             // ---------------------------------------------------------------- items and loads
             uint32_t it = 0, g = 0, asked = 0, answered = 0, qn[2] = {0, 0};
-            uint32_t x = blockIdx.x, y = blockIdx.y;
+            uint32_t x = blockIdx.x, unused;
             int row = 0;                    // of the tile being loaded
-            int32_t scan_b = 0;             // sequences before it have `scan_at` pairs of query tiles
-            uint32_t scan_at = 0;
+            // 32 sequences at a time, one to a lane: the first of them, the blocks before theirs, their lengths, the most
+            // tiles that one of their queries sees and their number of pairs of query tiles
+            int scan_b = 0, nqs = 0, nks = 0, deepest = 0;
+            uint32_t scan_at = 0, all = 0;
             bool ok = true, more = true;
-            const auto pairs = [&](int b) {
+            const auto look_at = [&](int b) {
                 int64_t first;
-                return b < a.B ? (mla::seq_rows(a.cu_q, a.Tq, a.B, b, first, a.flags) + 2 * ROWS - 1) / (2 * ROWS) : 0;
+                scan_b = b;
+                nqs = b + lane < a.B ? mla::seq_rows(a.cu_q, a.Tq, a.B, b + lane, first, a.flags) : 0;
+                nks = b + lane < a.B ? mla::seq_rows(a.cu_k, a.Tk, a.B, b + lane, first, a.flags) : 0;
+                deepest = __reduce_max_sync(0xffffffffu, (nks + ROWS - 1) / ROWS);
+                all = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(pairs_of(nqs)));
             };
+            // of this lane's sequence, the pairs that see v tiles or more; they are its last ones
+            const auto pairs_with = [&](int v) {
+                if (v == 0) return pairs_of(nqs);
+                const int64_t keys = static_cast<int64_t>(v - 1) * ROWS;  // more than these
+                if (!a.causal) return nks > keys ? pairs_of(nqs) : 0;
+                const int64_t t = keys - nks + nqs;  // a pair's end must lie behind query t
+                return t >= nqs ? 0 : pairs_of(nqs) - static_cast<int>(max(t, static_cast<int64_t>(0)) / (2 * ROWS));
+            };
+            look_at(0);
             while (ok) {
-                // block x is pair number x of query tiles, numbered over the sequences, the last pair of each (which sees the
-                // most keys) first; the grid may have more blocks than there are pairs
+                // The blocks are, for 32 sequences at a time, their pairs of query tiles and heads in LEVELS steps by the tiles
+                // that a pair sees, most first, so that what is left to the end is short (with one head after another CTAs
+                // stood idle for a tenth of 8,192 x 32 heads); in a step a head's pairs follow one another, as they share
+                // keys and values.  The grid may have more blocks than there are pairs.
                 Item w{};
-                if (x < scan_at) scan_b = scan_at = 0;
-                while (more && scan_b < a.B && !w.real) {
-                    const int p = pairs(scan_b + lane);
-                    int upto = p;
+                while (more && x >= scan_at + all * a.H && scan_b + 32 < a.B) {
+                    scan_at += all * a.H;
+                    look_at(scan_b + 32);
+                }
+                const uint32_t in = x - scan_at;
+                if (more && in < all * a.H) {
+                    const int step = max(1, (deepest + LEVELS - 1) / LEVELS);
+                    int v = step * (LEVELS - 1) + 1, later = 0;  // the step's least tiles; the sequence's pairs that see more
+                    uint32_t before = 0, upto;                   // pairs of all sequences before it, and with it
+                    while (true) {
+                        upto = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(pairs_with(v)));
+                        if (in < upto * a.H || v == 0) break;
+                        before = upto;
+                        later = pairs_with(v);
+                        v = max(v - step, 0);
+                    }
+                    const uint32_t n = upto - before, at = (in - before * a.H) % n;  // of n pairs of each head
+                    const int p = pairs_with(v) - later;
+                    int sum = p;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
-                        const int v = __shfl_up_sync(0xffffffffu, upto, d);
-                        if (lane >= d) upto += v;
+                        const int u = __shfl_up_sync(0xffffffffu, sum, d);
+                        if (lane >= d) sum += u;
                     }
-                    const uint32_t has = __ballot_sync(0xffffffffu, x < scan_at + upto);
-                    if (has) {
-                        const int l = __ffs(has) - 1, b = scan_b + l;
-                        const int mine = __shfl_sync(0xffffffffu, p, l), before = __shfl_sync(0xffffffffu, upto, l) - mine;
-                        int64_t first;
-                        w.real = 1;
-                        w.nq = mla::seq_rows(a.cu_q, a.Tq, a.B, b, first, a.flags);
-                        w.q0 = static_cast<int>(first);
-                        w.nk = mla::seq_rows(a.cu_k, a.Tk, a.B, b, first, a.flags);
-                        w.k0 = static_cast<int>(first);
-                        w.i0 = (mine - 1 - static_cast<int>(x - scan_at - before)) * 2 * ROWS;
-                        w.head = y;
-                    } else {
-                        scan_at += __shfl_sync(0xffffffffu, upto, 31);
-                        scan_b += 32;
-                    }
+                    const int l = __ffs(__ballot_sync(0xffffffffu, at < static_cast<uint32_t>(sum))) - 1;
+                    const int i = pairs_of(nqs) - 1 - later - (static_cast<int>(at) - (sum - p));
+                    int64_t first;
+                    w.real = 1;
+                    w.head = static_cast<int>((in - before * a.H) / n);
+                    w.i0 = __shfl_sync(0xffffffffu, i, l) * 2 * ROWS;
+                    w.nq = mla::seq_rows(a.cu_q, a.Tq, a.B, scan_b + l, first, a.flags);
+                    w.q0 = static_cast<int>(first);
+                    w.nk = mla::seq_rows(a.cu_k, a.Tk, a.B, scan_b + l, first, a.flags);
+                    w.k0 = static_cast<int>(first);
                 }
                 if (w.real || !more) {  // told to the other roles: an item, or that there are no more
                     ok = wait(&c.item_empty[it & 1], ((it >> 1) & 1) ^ 1);
@@ -438,7 +473,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ok = ok && wait(&c.taken_full, answered & 1);
                 if (!ok) break;
                 ++answered;
-                more = block_taken(&c.taken, x, y);
+                more = block_taken(&c.taken, x, unused);
+                if (more && x < scan_at) {
+                    scan_at = 0;
+                    look_at(0);
+                }
                 fence_async_smem();  // read before the next answer is written there
                 __syncwarp();
             }
@@ -612,7 +651,8 @@ cudaError_t launch(const MlaPrefillArgs& a) {
     // at most this many pairs of query tiles, wherever the sequences end
     const int64_t pairs = a.cu_q ? a.Tq / (2 * ROWS) + std::min<int64_t>(a.B, a.Tq)
                                  : a.B * ((a.Tq / a.B + 2 * ROWS - 1) / (2 * ROWS));
-    kernel<<<dim3(static_cast<unsigned>(pairs), a.H), THREADS, SMEM_BYTES, a.stream>>>(mq, mk, mv, mp, a);
+    if (pairs * a.H > INT32_MAX) return cudaErrorInvalidConfiguration;  // more queries than memory holds
+    kernel<<<static_cast<unsigned>(pairs * a.H), THREADS, SMEM_BYTES, a.stream>>>(mq, mk, mv, mp, a);
     return cudaGetLastError();
 }
 
