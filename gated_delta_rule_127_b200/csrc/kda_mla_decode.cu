@@ -54,7 +54,11 @@ struct Shape {
     static constexpr int NQ = E4M3 ? 2 * R : R;            // columns of the latent products (two parts for e4m3)
     static constexpr int BLOCKS = E4M3 ? 4 : 8;            // 128-byte column blocks of a latent row
     static constexpr int BLK = TOK * 128;                  // one block of a tile
-    static constexpr int PIECE = 4 * BLK;                  // four blocks of latents: the ring's unit
+    // Four blocks of latents, the ring's unit, as 8 groups of 8 tokens with 4 blocks of 1 KB each: then one box brings the
+    // four blocks of a page of any size, and 8-token groups lie evenly apart for the products.  (As four blocks of 64
+    // tokens, a tile of 16-token pages took 24 copies.)
+    static constexpr int PIECE = 4 * BLK;
+    static constexpr int ATOM = 1024, GROUP = 4 * ATOM;
     static constexpr int NP = BLOCKS / 4;                  // pieces of a tile
     static constexpr int PIECES = R == 32 ? 5 : 4;
     static constexpr int PES = R == 32 ? 3 : 2;            // tiles of positional keys
@@ -304,8 +308,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
         if (warp == 8) {
             // ---------------------------------------------------------------- loads
-            // A tile's copies: per page slot of up to 64 tokens the latent blocks (one box of four where a page holds the
-            // whole tile), the positional keys and the scales, each as soon as its place in the ring is free.  A tile's
+            // A tile's copies: per page slot of up to 64 tokens the latent blocks (a box of four), the positional keys and the scales, each as soon as its place in the ring is free.  A tile's
             // page numbers are read, by all lanes alike, a tile ahead.  (One lane per slot and shuffles: 1,500 cycles a
             // tile, as shuffles queue behind the other warps' shared-memory traffic; that bound the e4m3 form.)
             const int shift = min(a.cache.page_shift, 6), prow = 1 << shift, slots = TOK >> shift;
@@ -352,14 +355,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 if (used >> x & 1u) {
-                                    unsigned char* dst = kv + x * prow * 128;
-                                    if (prow == TOK) {
-                                        tma_load_3d(dst, &tm_kv, 0, row[x], done * 4, &c.kv_full[slot]);
-                                    } else {
-#pragma unroll
-                                        for (int k = 0; k < 4; ++k)
-                                            tma_load_3d(dst + k * SH::BLK, &tm_kv, 0, row[x], done * 4 + k, &c.kv_full[slot]);
-                                    }
+                                    tma_load_4d(kv + x * prow * 512, &tm_kv, 0, 0, done * 4, row[x] >> 3, &c.kv_full[slot]);
                                     if (done == 0) {
                                         tma_load_3d(smem + SH::OFF_PE + at_pe * SH::BLK + x * prow * 128, &tm_pe, 0, row[x], 0,
                                                     &c.kv_full[slot]);
@@ -414,13 +410,13 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     uint64_t k0[SH::NP];
 #pragma unroll
                     for (int h = 0; h < SH::NP; ++h)
-                        k0[h] = sw128_desc(base + (g * SH::NP + h) % SH::PIECES * SH::PIECE, 16, 1024);
+                        k0[h] = sw128_desc(base + (g * SH::NP + h) % SH::PIECES * SH::PIECE, 16, SH::GROUP);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < SH::BLOCKS; ++k)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint64_t da = k0[k / 4] + ((k % 4 * SH::BLK + j * 32) >> 4);
+                                const uint64_t da = k0[k / 4] + ((k % 4 * SH::ATOM + j * 32) >> 4);
                                 const uint64_t db = q0 + ((k * SH::NQ * 128 + j * 32) >> 4);
                                 if (E4M3) mma_f8(d, da, db, idesc_s, k + j > 0);
                                 else mma_f16(d, da, db, idesc_s, k + j > 0);
@@ -461,7 +457,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                     for (int h = 0; h < SH::NP; ++h) {
                         at[h] = (g * SH::NP + h) % SH::PIECES;
-                        v0[h] = sw128_desc(base + at[h] * SH::PIECE, SH::BLK, 1024);
+                        v0[h] = sw128_desc(base + at[h] * SH::PIECE, SH::ATOM, SH::GROUP);
                     }
                     if (elect_one()) {
 #pragma unroll
@@ -470,10 +466,10 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             for (int k = 0; k < (E4M3 ? 2 : 4); ++k) {
                                 const uint32_t d = tm + SH::COL_O + ch * SH::NQ;
                                 const uint64_t pk = ps + ((k * (E4M3 ? 32 : 16) * SH::PROW) >> 4);
-                                if (E4M3)  // 32 tokens of 128 channels: four groups of 8 tokens, 1024 bytes each
-                                    mma_f8(d, v0[0] + ((ch * SH::BLK + k * 4096) >> 4), pk, idesc_o, i > 0 || k > 0);
+                                if (E4M3)  // 32 tokens of 128 channels
+                                    mma_f8(d, v0[0] + ((ch * SH::ATOM + k * 4 * SH::GROUP) >> 4), pk, idesc_o, i > 0 || k > 0);
                                 else       // 16 tokens of 2 x 64 channels
-                                    mma_f16(d, v0[ch / (4 / SH::NP)] + ((ch % 2 * 2 * SH::BLK + k * 2048) >> 4), pk, idesc_o, i > 0 || k > 0);
+                                    mma_f16(d, v0[ch / (4 / SH::NP)] + ((ch % 2 * 2 * SH::ATOM + k * 2 * SH::GROUP) >> 4), pk, idesc_o, i > 0 || k > 0);
                             }
                             if (ch % (4 / SH::NP) == 4 / SH::NP - 1) mma_commit(&c.kv_empty[at[ch / (4 / SH::NP)]]);
                         }
@@ -632,10 +628,10 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         if (!seen && half == 0) {
 #pragma unroll 1
                             for (int k = wg; k < SH::BLOCKS; k += 2) {
-                                unsigned char* blk = smem + (g * SH::NP + k / 4) % SH::PIECES * SH::PIECE + k % 4 * SH::BLK;
+                                unsigned char* at = smem + (g * SH::NP + k / 4) % SH::PIECES * SH::PIECE + (tok >> 3) * SH::GROUP + k % 4 * SH::ATOM;
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)  // neighbouring tokens' stores in different banks
-                                    *reinterpret_cast<uint4*>(blk + tok * 128 + ((j + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                    *reinterpret_cast<uint4*>(at + (tok & 7) * 128 + ((j + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
                             }
                         }
                     }
@@ -973,16 +969,22 @@ bool encode_q(CUtensorMap* m, const void* q, int d, int rows, int B, int R) {
     return encode(m, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box);
 }
 
-// A cache array [pool rows, row_bytes] as {128 bytes, pool rows, blocks}.
-bool encode_pool(CUtensorMap* m, const void* base, int esize, int64_t pool_rows, int blocks, int box_rows,
-                 int box_blocks) {
-    const cuuint64_t inner = static_cast<cuuint64_t>(128 / esize);
-    const cuuint64_t dims[3] = {inner, static_cast<cuuint64_t>(pool_rows), static_cast<cuuint64_t>(blocks)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(blocks) * 128, 128};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(box_rows),
-                               static_cast<cuuint32_t>(box_blocks)};
-    return encode(m, base, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims,
+// Cached latents [pool rows, blocks of 128 bytes] as {128 bytes, 8 rows, blocks, pool rows / 8}: one box is four blocks of
+// box_rows tokens, 8 tokens after another.
+bool encode_latent(CUtensorMap* m, const void* base, int esize, int64_t pool_rows, int blocks, int box_rows) {
+    const cuuint64_t inner = static_cast<cuuint64_t>(128 / esize), row = static_cast<cuuint64_t>(blocks) * 128;
+    const cuuint64_t dims[4] = {inner, 8, static_cast<cuuint64_t>(blocks), static_cast<cuuint64_t>(pool_rows / 8)};
+    const cuuint64_t strides[3] = {row, 128, row * 8};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), 8, 4, static_cast<cuuint32_t>(box_rows / 8)};
+    return encode(m, base, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims,
                   strides, box);
+}
+
+// Cached positional keys [pool rows, 64] as {64, pool rows, 1}.
+bool encode_pe(CUtensorMap* m, const void* base, int64_t pool_rows, int box_rows) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(pool_rows), 1}, strides[2] = {128, 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+    return encode(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box);
 }
 
 template <int R, bool E4M3, typename TO>
@@ -997,12 +999,12 @@ cudaError_t launch(const MlaDecodeArgs& a, const Grid& g) {
     const int rows = a.S * a.H, box = a.cache.page_size < TOK ? a.cache.page_size : TOK;
     // a cache without pages is never loaded from (every page number is out of range): any valid map serves
     const bool none = a.cache.num_pages == 0;
-    const int64_t pool = none ? 1 : a.cache.num_pages * a.cache.page_size;
+    const int64_t pool = none ? 8 : a.cache.num_pages * a.cache.page_size;
     const void* latent = none ? a.q_latent : a.cache.latent;
     const void* cpe = none ? a.q_pe : a.cache.pe;
     if (!encode_q(&q, a.q_latent, kMlaLatent, rows, a.B, R) || !encode_q(&qp, a.q_pe, kMlaPe, rows, a.B, R) ||
-        !encode_pool(&kv, latent, E4M3 ? 1 : 2, pool, SH::BLOCKS, box, box == TOK ? 4 : 1) ||
-        !encode_pool(&pe, cpe, 2, pool, 1, box, 1))
+        !encode_latent(&kv, latent, E4M3 ? 1 : 2, pool, SH::BLOCKS, box) ||
+        !encode_pe(&pe, cpe, pool, box))
         return cudaErrorInvalidValue;
     const int ctas = g.groups * g.row_tiles;
     err = launch_early(kernel, dim3(ctas), dim3(THREADS), smem, a.stream, q, qp, kv, pe, a, g.row_tiles, g.groups);
