@@ -27,6 +27,11 @@
 // the most sequences finished 20% after the median of a batch of 128).  A sequence that a cut falls into leaves
 // partial (m, l, O) in the workspace, which mla_combine_kernel joins in a fixed order.  The cuts are found on the device from seq_lens, so a captured call follows new lengths.
 //
+// Bound by memory.  Measured: one sequence of 1,000,001 tokens, 32 heads, bf16 188 us (6.1 TB/s); 64 of 1,024 to 16,384
+// tokens 129 us (5.4 TB/s; 5.9 while this kernel runs); 128 of 1 to 8,000 tokens, 2 x 16 rows, e4m3, pages of 16 82 us
+// (4.3 TB/s).  What is over the copy rate: 4 us until the first loads, 8,000 cycles where a CTA passes from one sequence to
+// the next and its rings stand full, 7 us from the first CTA's end to the joined result.
+//
 // Roles of a CTA's 11 warps: 0-3 and 4-7 softmax, rescaling and output, each group of four for half of the rows and
 // independent of the other (thread = token, then channel); 8 loads (TMA); 9 issues the first products, 10 the second
 // ones (issuing 16 to 36 of them takes as long as they run: one warp for both would keep a tile's finished weights

@@ -287,6 +287,8 @@ KDA_API kda_status kda_decode_step_ex(const void* q, const void* k, const void* 
  * KDA_DEVFLAG_SEQ_LENS or KDA_DEVFLAG_PAGE_TABLE; nothing outside the given arrays is touched.  The rows of
  * a sequence skipped for its length (kda_mla_decode) or its cu_seqlens_k (kda_mla_prefill) get o = 0,
  * lse = -infinity; those of a sequence with bad cu_seqlens_q are left as they were.
+ * An infinity or NaN in a key, value or cached token stays within its sequence, but there can reach rows that do
+ * not see it (a weight of 0 times it is NaN).  What lies behind a sequence's last token may be anything.
  */
 
 /*

@@ -163,3 +163,20 @@ def test_no_queries():
     q, kv, kp = _inputs(0, 10, 2)
     o, lse = _run(q, kv, kp, [0], [10])
     assert o.shape == (0, 2, DV) and lse.shape == (0, 2)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_sequences_than_are_ordered_at_once(causal):
+    # the work is ordered by size 32 sequences at a time: lengths from 0 to several tiles, keys fewer and more than
+    # queries, on both sides of that boundary; a result nobody wrote would stay NaN
+    g = torch.Generator().manual_seed(13)
+    nq = torch.randint(0, 300, (70,), generator=g).tolist()
+    nk = [max(0, n + int(x)) for n, x in zip(nq, torch.randint(-150, 250, (70,), generator=g))]
+    nq[5], nk[5], nq[31], nk[31], nq[32], nk[32], nq[69], nk[69] = 900, 900, 600, 2000, 257, 0, 700, 1500
+    q, kv, kp = _inputs(sum(nq), sum(nk), 3)
+    o = torch.full((sum(nq), 3, DV), float("nan"), device=DEV)
+    lse = torch.full((sum(nq), 3), float("nan"), device=DEV)
+    kda.kda_mla_prefill(q, kv, kp, cu_of(nq, DEV), cu_of(nk, DEV), causal=causal, softmax_scale=SCALE, o=o, lse=lse)
+    want, tol, wl, lt = mla_ref.prefill(q, kv, kp, nq, nk, causal, SCALE, torch.float32)
+    check(o, want, tol, "o")
+    check(lse, wl, lt, "lse")
