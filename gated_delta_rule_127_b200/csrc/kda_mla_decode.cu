@@ -25,7 +25,8 @@
 // few tiles' worth added before each sequence for what it costs to begin and end one (queries, first maxima, output:
 // about 8,000 cycles against 1,800 per e4m3 tile, 6,000 against 3,200 per bf16 tile; without it the CTAs with
 // the most sequences finished 20% after the median of a batch of 128).  A sequence that a cut falls into leaves
-// partial (m, l, O) in the workspace, which mla_combine_kernel joins in a fixed order.  The cuts are found on the device from seq_lens, so a captured call follows new lengths.
+// partial (m, l, O) in the workspace, which mla_combine_kernel joins in a fixed order.  The cuts are found on the device
+// from seq_lens, so a captured call follows new lengths.
 //
 // Bound by memory.  Measured: one sequence of 1,000,001 tokens, 32 heads, bf16 188 us (6.1 TB/s); 64 of 1,024 to 16,384
 // tokens 129 us (5.4 TB/s; 5.9 while this kernel runs); 128 of 1 to 8,000 tokens, 2 x 16 rows, e4m3, pages of 16 82 us
@@ -313,9 +314,10 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
         if (warp == 8) {
             // ---------------------------------------------------------------- loads
-            // A tile's copies: per page slot of up to 64 tokens the latent blocks (a box of four), the positional keys and the scales, each as soon as its place in the ring is free.  A tile's
-            // page numbers are read, by all lanes alike, a tile ahead.  (One lane per slot and shuffles: 1,500 cycles a
-            // tile, as shuffles queue behind the other warps' shared-memory traffic; that bound the e4m3 form.)
+            // A tile's copies: per page slot of up to 64 tokens the latent blocks (a box of four), the positional keys and
+            // the scales, each as soon as its place in the ring is free.  A tile's page numbers are read, by all lanes
+            // alike, a tile ahead.  (One lane per slot and shuffles took 1,500 cycles a tile, as shuffles queue behind the
+            // other warps' shared-memory traffic, and bound the e4m3 form.)
             const int shift = min(a.cache.page_shift, 6), prow = 1 << shift, slots = TOK >> shift;
             uint32_t g = 0, n = 0;  // tiles and pieces issued
             bool ok = true;
@@ -325,8 +327,9 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     const int pos = (w.t + i) * TOK;
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        page[x] = x < slots && i < w.n && pos + x * prow < w.len ? __ldg(table + ((pos + x * prow) >> a.cache.page_shift))
-                                                                                 : 0;
+                        page[x] = x < slots && i < w.n && pos + x * prow < w.len
+                                      ? __ldg(table + ((pos + x * prow) >> a.cache.page_shift))
+                                      : 0;
                 };
                 int page[4];
                 fetch(page, 0);
