@@ -163,3 +163,34 @@ def test_calls_wait_for_what_comes_before(last, captured):
         assert torch.equal(out[1], new[i][0]) and torch.equal(pe, new[i][1])
         want, tol, _, _ = mla_ref.decode(new[i][2], new[i][3], cache, SCALE, BF16)
         mla_ref.check(got, want, tol, "o")
+
+
+def test_two_streams_at_once():
+    # two caches and two workspaces, each call's results as when it ran alone
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    caches = [Cache([700, 1, 90], 64, BF16, DEV, seed=1).fill(5), Cache([33, 2000], 16, torch.float8_e4m3fn, DEV, seed=2).fill(6)]
+    g = torch.Generator(device=DEV).manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)  # noqa: E731
+    work = []
+    for c in caches:
+        B = len(c.lengths)
+        work.append(dict(q=[r(B, 1, 32, LATENT) for _ in range(10)], p=[r(B, 1, 32, PE) for _ in range(10)],
+                         lat=r(B, LATENT), pe=r(B, PE), cu=cu_of([1] * B, DEV)))
+
+    def run(c, w):
+        kda.kda_mla_cache_write(w["lat"], w["pe"], c.latent, c.pe, c.table, c.seq_lens, w["cu"], cache_scale=c.scale)
+        return [kda.kda_mla_decode(q, p, c.latent, c.pe, c.table, c.seq_lens, softmax_scale=SCALE, cache_scale=c.scale,
+                                   output_lse=True) for q, p in zip(w["q"], w["p"])]
+
+    alone = [run(c, w) for c, w in zip(caches, work)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [None, None]
+        for i, s in enumerate(streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got[i] = run(caches[i], work[i])
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            for (o1, l1), (o2, l2) in zip(a, b):
+                assert torch.equal(o1, o2) and torch.equal(l1, l2)
