@@ -2,6 +2,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "kda.h"
 #include "kda_internal.h"
@@ -16,6 +17,26 @@ bool given16(const void* p) { return p && aligned16(p); }
 
 // Rows and positions are 32-bit numbers in the kernels, also those just past a last tile of 256.
 constexpr int64_t kMostRows = 0x7fffff00;
+
+// An array of a call.  Kernels read inputs while others of their blocks write, so an output may lie over nothing else.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span* other = outputs.begin(); other != o; ++other)
+            if (overlap(*o, *other)) return false;
+        for (const Span& i : inputs)
+            if (overlap(*o, i)) return false;
+    }
+    return true;
+}
+int64_t size_of(kda_dtype d) { return d == KDA_FP32 ? 4 : d == KDA_BF16 ? 2 : 1; }
 
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
@@ -52,6 +73,11 @@ kda_status check_cache(const void* latent, const void* pe, const float* scale, c
     return KDA_OK;
 }
 
+Span latent_of(const MlaCache& c) { return {c.latent, c.num_pages * c.page_size * kMlaLatent * (c.e4m3 ? 1 : 2)}; }
+Span pe_of(const MlaCache& c) { return {c.pe, c.num_pages * c.page_size * kMlaPe * 2}; }
+Span scale_of(const MlaCache& c) { return {c.scale, c.num_pages * c.page_size * 4}; }
+Span table_of(const MlaCache& c, int B) { return {c.page_table, static_cast<int64_t>(B) * c.max_pages * 4}; }
+
 kda_status status_of(cudaError_t err) { return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 kda_status cache_copy(bool write, const void* latent, const void* pe, const int32_t* cu_seqlens, const int32_t* lens,
@@ -59,6 +85,11 @@ kda_status cache_copy(bool write, const void* latent, const void* pe, const int3
     if (T == 0) return KDA_OK;
     if (!given16(latent) || !given16(pe)) return KDA_ERR_INVALID_ARG;
     if ((write && !lens) || !aligned4(lens) || !aligned4(cu_seqlens)) return KDA_ERR_INVALID_ARG;
+    const Span rows{latent, T * kMlaLatent * size_of(dtype)}, keys{pe, T * kMlaPe * size_of(dtype)};
+    const Span cu{cu_seqlens, (static_cast<int64_t>(B) + 1) * 4}, each{lens, static_cast<int64_t>(B) * 4};
+    const Span cl = latent_of(cache), cp = pe_of(cache), cs = scale_of(cache), table = table_of(cache, B);
+    if (write ? !apart({cl, cp, cs}, {rows, keys, cu, each, table}) : !apart({rows, keys}, {cl, cp, cs, cu, each, table}))
+        return KDA_ERR_INVALID_ARG;
     MlaCacheCopyArgs a{};
     a.cache = cache;
     a.latent = const_cast<void*>(latent);
@@ -137,6 +168,12 @@ kda_status kda_mla_decode(const void* q_latent, const void* q_pe, const void* ca
     const bool have_ws = workspace != nullptr && workspace_bytes > 0;
     if (have_ws && (!aligned16(workspace) || workspace_bytes < mla_decode_workspace_size(B, S, H)))
         return KDA_ERR_INVALID_ARG;
+    const int64_t q_rows = static_cast<int64_t>(B) * S * H;
+    if (!apart({{o, q_rows * kMlaLatent * size_of(dtype_o)}, {lse, q_rows * 4},
+                {have_ws ? workspace : nullptr, static_cast<int64_t>(mla_decode_workspace_size(B, S, H))}},
+               {{q_latent, q_rows * kMlaLatent * 2}, {q_pe, q_rows * kMlaPe * 2}, latent_of(c), pe_of(c), scale_of(c),
+                table_of(c, B), {seq_lens, static_cast<int64_t>(B) * 4}}))
+        return KDA_ERR_INVALID_ARG;
     MlaDecodeArgs a{};
     a.q_latent = q_latent;
     a.q_pe = q_pe;
@@ -171,6 +208,11 @@ kda_status kda_mla_prefill(const void* q, const void* kv, const void* k_pe, cons
     if (!given16(q) || !given16(o) || !aligned4(lse) || !aligned4(cu_seqlens_q) || !aligned4(cu_seqlens_k))
         return KDA_ERR_INVALID_ARG;
     if (Tk > 0 && (!given16(kv) || !given16(k_pe))) return KDA_ERR_INVALID_ARG;
+    const int64_t cu_bytes = (static_cast<int64_t>(B) + 1) * 4;
+    if (!apart({{o, Tq * H * kMlaV * size_of(dtype_o)}, {lse, Tq * H * 4}},
+               {{q, Tq * H * kMlaQk * 2}, {kv, Tk * H * kMlaKv * 2}, {k_pe, Tk * kMlaPe * 2}, {cu_seqlens_q, cu_bytes},
+                {cu_seqlens_k, cu_bytes}}))
+        return KDA_ERR_INVALID_ARG;
     MlaPrefillArgs a{};
     a.q = q; a.kv = kv; a.k_pe = k_pe;
     a.cu_q = cu_seqlens_q; a.cu_k = cu_seqlens_k;

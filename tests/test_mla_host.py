@@ -144,3 +144,43 @@ def test_binding_refuses_shapes_and_types():
         kda.kda_mla_prefill(q, kv, kp, softmax_scale=0.1, lse=torch.zeros(8))
     with pytest.raises(ValueError, match="CUDA tensor"):
         kda.kda_mla_prefill(q, kv, kp, softmax_scale=0.1)
+
+
+# Calls whose arrays lie apart but for one pair.  They are refused before anything is launched; where that failed they
+# would run on fake addresses, so only machines without a GPU make them.
+def _far(k):
+    return (k + 1) << 36
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses")
+@pytest.mark.parametrize("kw", [
+    dict(o=_far(0)), dict(o=_far(0) + 2 * 32 * 512 * 2 - 16), dict(o=_far(1)), dict(o=_far(2) + 16), dict(o=_far(3)),
+    dict(lse=_far(0) + 64), dict(lse=_far(4)), dict(lse=_far(5)), dict(lse=_far(6) + 64),
+    dict(ws=_far(0), wsb=1 << 30), dict(ws=_far(6) - 1024, wsb=1 << 30),
+    dict(dc=kda.KDA_E4M3, cs=_far(9), lse=_far(9) + 4 * 64 * 4 - 4),
+])
+def test_decode_refuses_outputs_over_other_arrays(lib, kw):
+    apart = dict(q=_far(0), qp=_far(1), cl=_far(2), cp=_far(3), table=_far(4), lens=_far(5), o=_far(6), lse=_far(7))
+    assert _decode(lib, **{**apart, **kw}) == INV
+    assert _decode(lib, **apart) == kda.KDA_ERR_CUDA  # apart: refused only for want of a GPU
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses")
+@pytest.mark.parametrize("kw", [dict(o=_far(0)), dict(o=_far(0) + 8 * 4 * 192 * 2 - 16), dict(o=_far(1)), dict(o=_far(2)),
+                                dict(lse=_far(0)), dict(lse=_far(5)), dict(lse=_far(3), cq=_far(3)), dict(o=_far(4), ck=_far(4), cq=_far(3))])
+def test_prefill_refuses_outputs_over_other_arrays(lib, kw):
+    apart = dict(q=_far(0), kv=_far(1), kp=_far(2), o=_far(5), lse=_far(6))
+    assert _prefill(lib, **{**apart, **kw}) == INV
+    assert _prefill(lib, **apart) == kda.KDA_ERR_CUDA
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses")
+@pytest.mark.parametrize("kw", [dict(latent=_far(2)), dict(pe=_far(3) + 4 * 64 * 128 - 16), dict(latent=_far(3)),
+                                dict(dc=kda.KDA_E4M3, cs=_far(0) + 16), dict(table=_far(2)), dict(cl=_far(3) - 16)])
+def test_cache_calls_refuse_outputs_over_other_arrays(lib, kw):
+    apart = dict(latent=_far(0), pe=_far(1), cl=_far(2), cp=_far(3), table=_far(4))
+    assert _write(lib, **{**apart, "lens": _far(5), **kw}) == INV
+    assert _write(lib, **{**apart, "lens": _far(5)}) == kda.KDA_ERR_CUDA
+    if "table" not in kw and "cl" not in kw:
+        assert _read(lib, **{**apart, "starts": _far(5), **kw}) == INV
+    assert _read(lib, **{**apart, "starts": _far(5)}) == kda.KDA_ERR_CUDA
