@@ -18,8 +18,18 @@
 // multiplies its scores after the product and its weight before it; the reference m is the maximum of
 // x + log2(s) less 4, so the weights w s that enter the product lie in [0, 2^8.5].
 //
-// The reference moves only when a new maximum exceeds it by 8 (bf16) or 4.5 + 4 (e4m3) in log2 units; then the
+// The reference rises only when a new maximum exceeds it by 8 (bf16) or 4.5 + 4 (e4m3) in log2 units; then the
 // accumulated output and sums are multiplied by 2^(old - new).  Until then weights above 1 are as exact as any.
+//
+// e4m3: it falls, too.  The two parts end at 2^-13: a small w s is off by up to 2^-14, and below that it is 0.  Under a
+// reference that only rises, one heavy token (2^4) takes the tail of a long sequence out of the output while l still
+// counts it: 5% of the output for 131,072 tokens 13 nats below the first one.  So every 8 tiles (and once early, as the
+// heavy token is mostly the first) each row looks at what the tokens since the last look weigh, e = sum w s.  From 8 on, their
+// 512 x 2^-14 are 2^-8 of that at most, as much as the rounding of a bf16 weight.  Below, the reference falls to where they
+// would have weighed 16 to 32: then what they have lost is at most 2^-9 of the heavy token's 2^4, each time a quarter of the
+// time before.  At most 20 below its highest place: there 2^30 tokens that weigh nothing are 2^-8 of that token, and O and l
+// stay far from fp32's end.  A look takes some 300 cycles beside a tile's 1,800: with looks at every 4th, 8th and 16th tile
+// one sequence of 1,000,001 tokens took 141, 138 and 137 us, without any 136.
 //
 // Work split: all tiles of all sequences, in order, are cut into G equal ranges, one per CTA (per row tile), with a
 // few tiles' worth added before each sequence for what it costs to begin and end one (queries, first maxima, output:
@@ -96,6 +106,8 @@ struct Ctl {
     alignas(16) float qscale[E4M3 ? R : 4];      // e4m3: the query rows' scales
     alignas(16) float red[4][R];          // per warp and row: maxima; at a segment's end sums
     alignas(16) float factor[R];                 // per row: rescaling factor; at a segment's end 1 / l
+    alignas(16) float mass[4][E4M3 ? R : 4];     // e4m3, per warp and row: what a window's tokens weigh
+    alignas(16) float lowest[E4M3 ? R : 4];      // e4m3, per row: where the reference may fall to
 };
 template <int R, bool E4M3>
 constexpr int kSmemBytes = Shape<R, E4M3>::OFF_CTL + static_cast<int>(sizeof(Ctl<R, E4M3>));
@@ -500,7 +512,8 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int bar = 1 + wg, h0 = wg * (R / 2) + half * HH;  // named barrier, first row of this thread
             const bool writer = sub == 0 && (lane & 15) == 0;
             const float sl2 = a.scale * 1.4426950408889634f;
-            constexpr float kOver = E4M3 ? 8.5f : 8.f, kBelow = E4M3 ? 4.f : 0.f;
+            constexpr float kOver = E4M3 ? 8.5f : 8.f, kBelow = E4M3 ? 4.f : 0.f, kFall = 20.f;
+            constexpr int kWindow = 8;  // e4m3: tiles between two looks at what the tokens weigh
             const uint32_t lane_base = static_cast<uint32_t>(sub * 32) << 16;
             unsigned char* p_tile = smem + SH::OFF_P;
             // this thread's first row: new token and head (rows past the sequence's own are never stored)
@@ -568,9 +581,12 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
 
             while (true) {
-                float m[HH], l[HH];
+                float m[HH], l[HH], e[E4M3 ? HH : 1] = {};  // e: what the tokens since the last look weigh
 #pragma unroll
                 for (int i = 0; i < HH; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+                if (E4M3 && writer)
+#pragma unroll
+                    for (int i = 0; i < HH; ++i) c.lowest[h0 + i] = -INFINITY;
                 if (E4M3 && w.left > w.n + SH::LEAD && row0 + (tid >> 3) < rows)  // the next segment's queries, into L2
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(
                         static_cast<const __nv_bfloat16*>(a.q_latent) +
@@ -648,8 +664,41 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     bool over = false;
 #pragma unroll
                     for (int i = 0; i < HH; ++i) over = over || x[i] + ls > m[i] + kOver;
-                    // (a failed wait takes the same way, to the barrier at which all four warps stop)
-                    const bool move = group_sync_or(bar, 128, over || !ok);
+                    // (A failed wait takes the same way, to the barrier at which all four warps stop.)  e4m3: the vote is also the
+                    // barrier of a look's sums.
+                    const bool look = E4M3 && t > 0 && (t % kWindow == 0 || t == 3);
+                    if constexpr (E4M3) {
+                        if (look) {
+                            reduce16<HH, false>(e, lane);
+                            c.mass[sub][h0 + (lane & 15) * HH / 16] = e[0];
+                        }
+                    }
+                    bool move = group_sync_or(bar, 128, over || !ok);
+                    [[maybe_unused]] uint32_t fall[2] = {0u, 0u};  // e4m3, a byte per row: by how much its reference falls
+                    if constexpr (E4M3) {
+                        static_assert(HH == 8 && kWindow == 8, "rows in `fall`, exponents below");
+                        if (look) {  // tiles 1 and 2: below 2, to 4 .. 8; kWindow tiles: below 8, to 16 .. 32
+                            const int most = 127 + (t == 3 ? 2 : 4);
+#pragma unroll
+                            for (int i = 0; i < HH; i += 4) {
+                                float4 r[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const float4*>(&c.mass[k][h0 + i]);
+                                const float mass[4] = {(r[0].x + r[1].x) + (r[2].x + r[3].x), (r[0].y + r[1].y) + (r[2].y + r[3].y),
+                                                       (r[0].z + r[1].z) + (r[2].z + r[3].z), (r[0].w + r[1].w) + (r[2].w + r[3].w)};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int by = most - static_cast<int>(__float_as_uint(mass[k]) >> 23);
+                                    if (by > 1) fall[i / 4] |= static_cast<uint32_t>(by) << (8 * k);
+                                }
+                            }
+                            move = __any_sync(0xffffffffu, (fall[0] | fall[1]) != 0u) || move;  // the same in all four warps
+                        }
+                        if (look || t == 1) {
+#pragma unroll
+                            for (int i = 0; i < HH; ++i) e[i] = 0.f;
+                        }
+                    }
                     if (move) {
                         float v[HH];
 #pragma unroll
@@ -659,11 +708,16 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         for (int i = 0; i < (HH + 15) / 16; ++i) c.red[sub][h0 + (lane & 15) * HH / 16 + i] = v[i];
                         stop = group_sync_or(bar, 128, !ok);
                         if (stop) break;
-                        // the accumulated output moves too: the last product must be done with it
-                        if (g > 0) ok = ok && wait(&c.pv_done, (g - 1) & 1);
-                        tc_fence_after_sync();
 #pragma unroll
                         for (int i = 0; i < HH; i += 4) {
+                            float to[4] = {m[i], m[i + 1], m[i + 2], m[i + 3]};
+                            if constexpr (E4M3) {
+                                const float4 low = *reinterpret_cast<const float4*>(c.lowest + h0 + i);
+                                const float least[4] = {low.x, low.y, low.z, low.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)  // (a row that has seen nothing has both at -infinity)
+                                    if (to[k] > least[k]) to[k] = fmaxf(to[k] - static_cast<float>(fall[i / 4] >> (8 * k) & 255u), least[k]);
+                            }
                             float4 r[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const float4*>(&c.red[k][h0 + i]);
@@ -674,18 +728,26 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             float f[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
+                                if (top[k] > to[k] + kOver) to[k] = top[k] - kBelow;
                                 f[k] = 1.f;
-                                if (top[k] > m[i + k] + kOver) {
-                                    f[k] = ex2(m[i + k] - (top[k] - kBelow));
-                                    m[i + k] = top[k] - kBelow;
+                                if (to[k] != m[i + k]) {
+                                    f[k] = ex2(m[i + k] - to[k]);
+                                    m[i + k] = to[k];
                                     l[i + k] *= f[k];
+                                    if constexpr (E4M3) e[i + k] *= f[k];
                                 }
                             }
                             if (writer)
                                 *reinterpret_cast<float4*>(c.factor + h0 + i) = make_float4(f[0], f[1], f[2], f[3]);
                         }
                         group_sync(bar, 128);
+                        if (E4M3 && writer)  // read only before that barrier
+#pragma unroll
+                            for (int i = 0; i < HH; ++i) c.lowest[h0 + i] = fmaxf(c.lowest[h0 + i], m[i] - kFall);
                         if (t > 0) {
+                            // the accumulated output moves too: the last product must be done with it
+                            ok = ok && wait(&c.pv_done, (g - 1) & 1);
+                            tc_fence_after_sync();
 #pragma unroll 1
                             for (int k = 0; k < 4 * SH::NQ / R; ++k) {  // chunk and part: this group's half of the rows
                                 float o[R / 2];
@@ -710,6 +772,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     for (int i = 0; i < HH; ++i) {
                         x[i] = ex2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
                         l[i] += x[i];
+                        if constexpr (E4M3) e[i] = fmaf(x[i], ts, e[i]);
                     }
                     uint32_t pk[HH / 2];  // bf16: pairs of columns; e4m3: pairs of the high parts, then of the low ones
                     if constexpr (E4M3) {

@@ -336,7 +336,10 @@ KDA_API size_t kda_mla_decode_workspace_size(int B, int S, int H, int d_latent, 
  *   B >= 0 (0 launches nothing), S >= 1, H >= 1, S * H <= 65535
  * Arithmetic: products of bf16 values with fp32 accumulation; softmax statistics and the output are held in
  * fp32; the weights enter the second product in bf16.  With KDA_E4M3 the codes are multiplied as they are and
- * queries and weights enter as two e4m3 parts each, which carry as many bits as bf16.
+ * queries and weights enter as two e4m3 parts each: a value is off by at most 2^-8 of itself, as in bf16, or by an
+ * absolute amount where it is small: a query's channel by 2^-21 of its row's largest one, a weight times its
+ * token's scale by an amount that, over all tokens of a row however many, adds up to at most 2^-6 of the row's
+ * sum of (weight x scale) times the largest mean |code| of 512 neighbouring tokens.
  */
 KDA_API kda_status kda_mla_decode(const void* q_latent, const void* q_pe, const void* cache_latent,
                          const void* cache_pe, const float* cache_scale, const int32_t* page_table,
