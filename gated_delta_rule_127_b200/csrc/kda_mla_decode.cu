@@ -53,12 +53,15 @@
 
 #include "kda_mla_common.cuh"
 #include "kda_mla_sm100.cuh"
+#include "kda_mla_split.h"
 #include "kda_tma.h"
 
 namespace kda {
 namespace {
 
 using namespace sm100;
+using mla::group_of;
+using mla::scaled;
 
 constexpr int TOK = 64;          // tokens per tile
 constexpr int THREADS = 352;
@@ -144,18 +147,6 @@ __host__ __device__ inline Part part_of(void* ws, int ctas, int R) {
     p.m = p.o + static_cast<size_t>(ctas) * 2 * R * kMlaLatent;
     p.l = p.m + static_cast<size_t>(ctas) * 2 * R;
     return p;
-}
-
-// x a / b for 0 <= a, b <= GROUPS; the 64-bit division, some 400 cycles of latency, only for what 32 bits do not hold.
-__device__ __forceinline__ long long scaled(long long x, int a, int b) {
-    if (x < (1 << 24)) return static_cast<uint32_t>(x) * static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return x * a / b;
-}
-// The largest group whose range begins at or before `place`: (place + 1) groups - 1 over total.
-__device__ __forceinline__ int group_of(long long place, int groups, long long total) {
-    const long long n = (place + 1) * groups - 1;
-    if (n < (1ll << 32)) return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(total));
-    return static_cast<int>(n / total);
 }
 
 // A CTA's walk over its range of tiles: one segment per sequence it touches.
