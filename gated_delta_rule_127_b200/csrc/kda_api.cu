@@ -72,9 +72,9 @@ kda_status debug_check_batch(const int32_t* cu_seqlens, int64_t T_total, int N, 
     if (!cu_seqlens) return KDA_OK;
     std::vector<int32_t> cu(static_cast<size_t>(N) + 1);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemcpyAsync(cu.data(), cu_seqlens, cu.size() * sizeof(int32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return KDA_ERR_CUDA;
+    cudaError_t err = cudaMemcpyAsync(cu.data(), cu_seqlens, cu.size() * sizeof(int32_t), cudaMemcpyDeviceToHost, s);
+    if (err == cudaSuccess) err = cudaStreamSynchronize(s);
+    if (err != cudaSuccess) return status_of(err);
     if (cu[0] != 0 || cu[N] != T_total) return KDA_ERR_INVALID_ARG;
     const int64_t slots = wy::num_slots(T_total, N);
     for (int n = 0; n < N; ++n) {
@@ -147,7 +147,7 @@ kda_status chunk_fwd(const void* q, const void* k, const void* v, const void* lo
     a.epilogue = (options & KDA_OPT_OUTPUT_NORM_GATE) != 0;
     a.out_gate = out_gate; a.norm_weight = norm_weight; a.norm_eps = norm_eps;
     a.wait_polls = consumer_wait_polls();
-    if (device_flags_ptr(&a.flags) != cudaSuccess) return KDA_ERR_CUDA;
+    if (const kda_status st = status_of(device_flags_ptr(&a.flags)); st != KDA_OK) return st;
 #ifdef KDA_DEBUG
     if (const kda_status st = debug_check_batch(cu_seqlens, T_total, N, stream); st != KDA_OK) return st;
 #endif
@@ -164,7 +164,7 @@ kda_status chunk_fwd(const void* q, const void* k, const void* v, const void* lo
         err = launch_chunk_simt(a);
     }
     if (err == cudaSuccess && a.epilogue && !epilogue_fused) err = launch_output_epilogue(a);
-    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return status_of(err);
 }
 
 // kda_decode_step, kda_gdn_decode_step and kda_decode_step_ex (KDA_OPT_* options).
@@ -199,7 +199,7 @@ kda_status decode_step(const void* q, const void* k, const void* v, const void* 
     a.epilogue = (options & KDA_OPT_OUTPUT_NORM_GATE) != 0;
     a.out_gate = out_gate; a.norm_weight = norm_weight; a.norm_eps = norm_eps;
     NvtxRange range("kda_decode_step");
-    return launch_decode(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return status_of(launch_decode(a));
 }
 
 }  // namespace kda
@@ -269,13 +269,12 @@ kda_status kda_decode_step_ex(const void* q, const void* k, const void* v, const
 kda_status kda_get_device_status(void* stream, uint32_t* flags) {
     using namespace kda;
     if (flags) *flags = 0;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KDA_ERR_CUDA;
-    unsigned int* addr = nullptr;
-    if (device_flags_ptr(&addr) != cudaSuccess) return KDA_ERR_CUDA;
-    unsigned int value = 0, zero = 0;
-    if (cudaMemcpy(&value, addr, sizeof(value), cudaMemcpyDeviceToHost) != cudaSuccess) return KDA_ERR_CUDA;
-    if (value && cudaMemcpy(addr, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
-        return KDA_ERR_CUDA;
+    unsigned int *addr = nullptr, value = 0, zero = 0;
+    cudaError_t err = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (err == cudaSuccess) err = device_flags_ptr(&addr);
+    if (err == cudaSuccess) err = cudaMemcpy(&value, addr, sizeof(value), cudaMemcpyDeviceToHost);
+    if (err == cudaSuccess && value) err = cudaMemcpy(addr, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (err != cudaSuccess) return status_of(err);
     if (flags) *flags = value;
     if (value & KDA_DEVFLAG_TIMEOUT) return KDA_ERR_TIMEOUT;
     return value ? KDA_ERR_DEVICE_CHECK : KDA_OK;

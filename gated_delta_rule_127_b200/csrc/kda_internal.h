@@ -11,6 +11,13 @@
 
 namespace kda {
 
+// The status of a CUDA call.  An error is taken off the runtime's record, where the next launch's check would find it.
+inline kda_status status_of(cudaError_t err) {
+    if (err == cudaSuccess) return KDA_OK;
+    cudaGetLastError();
+    return KDA_ERR_CUDA;
+}
+
 struct ChunkArgs {
     const void* q;
     const void* k;

@@ -78,8 +78,6 @@ Span pe_of(const MlaCache& c) { return {c.pe, c.num_pages * c.page_size * kMlaPe
 Span scale_of(const MlaCache& c) { return {c.scale, c.num_pages * c.page_size * 4}; }
 Span table_of(const MlaCache& c, int B) { return {c.page_table, static_cast<int64_t>(B) * c.max_pages * 4}; }
 
-kda_status status_of(cudaError_t err) { return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
-
 kda_status cache_copy(bool write, const void* latent, const void* pe, const int32_t* cu_seqlens, const int32_t* lens,
                       int64_t T, int B, kda_dtype dtype, const MlaCache& cache, void* stream) {
     if (T == 0) return KDA_OK;
@@ -100,7 +98,7 @@ kda_status cache_copy(bool write, const void* latent, const void* pe, const int3
     a.B = B;
     a.fp32 = dtype == KDA_FP32;
     a.stream = static_cast<cudaStream_t>(stream);
-    if (device_flags_ptr(&a.flags) != cudaSuccess) return KDA_ERR_CUDA;
+    if (const kda_status st = status_of(device_flags_ptr(&a.flags)); st != KDA_OK) return st;
     NvtxRange range(write ? "kda_mla_cache_write" : "kda_mla_cache_read");
     return status_of(write ? launch_mla_cache_write(a) : launch_mla_cache_read(a));
 }
@@ -187,7 +185,7 @@ kda_status kda_mla_decode(const void* q_latent, const void* q_pe, const void* ca
     a.workspace = have_ws ? workspace : nullptr;
     a.wait_polls = consumer_wait_polls();
     a.stream = static_cast<cudaStream_t>(stream);
-    if (device_flags_ptr(&a.flags) != cudaSuccess) return KDA_ERR_CUDA;
+    if (const kda_status st = status_of(device_flags_ptr(&a.flags)); st != KDA_OK) return st;
     NvtxRange range("kda_mla_decode");
     return status_of(launch_mla_decode(a));
 }
@@ -225,7 +223,7 @@ kda_status kda_mla_prefill(const void* q, const void* kv, const void* k_pe, cons
     a.lse = lse;
     a.wait_polls = consumer_wait_polls();
     a.stream = static_cast<cudaStream_t>(stream);
-    if (device_flags_ptr(&a.flags) != cudaSuccess) return KDA_ERR_CUDA;
+    if (const kda_status st = status_of(device_flags_ptr(&a.flags)); st != KDA_OK) return st;
     NvtxRange range("kda_mla_prefill");
     return status_of(launch_mla_prefill(a));
 }

@@ -53,7 +53,8 @@ kda_status kda_chunk_fwd_static_scratch(const void* q, const void* k, const void
                             : 0;
     if (need > KDA_STATIC_SCRATCH_BYTES) return KDA_ERR_UNSUPPORTED;  // checked before any CUDA call
     void* scratch = nullptr;
-    if (need > 0 && kda::static_scratch_ptr(&scratch) != cudaSuccess) return KDA_ERR_CUDA;
+    if (need > 0)
+        if (const kda_status st = kda::status_of(kda::static_scratch_ptr(&scratch)); st != KDA_OK) return st;
     return kda_chunk_fwd(q, k, v, log_alpha, beta, initial_state, cu_seqlens, T_total, N, H, dk, dv, chunk_size,
                          dtype_qkv, dtype_gate, dtype_o, o, final_state, scratch,
                          need > 0 ? static_cast<size_t>(KDA_STATIC_SCRATCH_BYTES) : 0, stream);
