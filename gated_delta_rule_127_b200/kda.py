@@ -382,7 +382,10 @@ def _on_stream(fn):
             if stream is None:
                 return fn(*args, **kw)
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(_stream_handle(stream), first.device)
+                handle = _stream_handle(stream)
+                if handle == 1:  # cudaStreamLegacy, the default stream, which torch only knows as 0
+                    handle = 0
+                stream = torch.cuda.ExternalStream(handle, first.device)
             if stream.device != first.device:
                 raise ValueError(f"the stream belongs to {stream.device}, the tensors to {first.device}")
             with torch.cuda.stream(stream):
