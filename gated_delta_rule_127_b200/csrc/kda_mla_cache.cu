@@ -4,7 +4,8 @@
 // Per token: 512 latent channels and 64 positional ones.  e4m3: with a = max |c|, the scale is s = 2^k,
 // k = the least integer with a <= 448 2^k, clamped to [-64, 120]; codes are e4m3(c / s).  A power of two
 // makes c / s and code * s exact, so the only rounding is the one to e4m3 (half a step of 2^-4) and a value
-// read back is exact in bf16 too.
+// read back is exact in bf16 too.  One end: with s = 2^120 a code of 256 or more stands for 2^128 or more, which
+// fp32 and bf16 read as infinity (|c| from 248 x 2^120 = 3.30e38 on: the largest bf16, 3.39e38, and infinity itself).
 //
 // Both directions are bound by memory (a token moves 1152 B on the packed side and 644 or 1152 B on the cache's).  A warp
 // takes a token, or several with all their loads in flight: lane l holds channels 8 l .. 8 l + 7 and 256 + 8 l .. of the

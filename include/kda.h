@@ -314,6 +314,8 @@ KDA_API kda_status kda_mla_cache_write(const void* latent, const void* pe, const
  *   cu_seqlens how many tokens of each sequence, n_b, and where they go in the packed arrays
  *   starts     [B] int32 (device) or NULL (zeros): the positions read are starts[b] .. starts[b] + n_b - 1
  *   latent     [T, d_latent], pe [T, d_pe]  dtype_o (KDA_BF16 or KDA_FP32)
+ * Values are code times scale, exact in both types, but for those of 2^128 and more, which become infinite: what
+ * kda_mla_cache_write rounded to code 256 or more under the scale 2^120, from magnitudes of 3.30e38 on.
  * Rows of a skipped sequence and tokens of a bad page are left as they were.  T >= 0, B >= 1.
  */
 KDA_API kda_status kda_mla_cache_read(const void* cache_latent, const void* cache_pe, const float* cache_scale,
