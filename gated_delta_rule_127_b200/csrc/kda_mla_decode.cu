@@ -14,7 +14,7 @@
 //
 // e4m3: the codes are multiplied as they are (kind::f8f6f4).  Queries and weights enter as two e4m3 parts,
 // hi = e4m3(x) and lo = e4m3(16 (x - hi)), as 2 R columns of one product whose halves are added (hi + lo / 16) in
-// fp32: 4 + 4 significant bits, as many as bf16, without a pass that turns codes into bf16.  A token's scale s
+// fp32: 4 + 4 significant bits, as many as bf16 (down to 2^-6), without a pass that turns codes into bf16.  A token's scale s
 // multiplies its scores after the product and its weight before it; the reference m is the maximum of
 // x + log2(s) less 4, so the weights w s that enter the product lie in [0, 2^8.5].
 //
@@ -38,9 +38,9 @@
 // partial (m, l, O) in the workspace, which mla_combine_kernel joins in a fixed order.  The cuts are found on the device
 // from seq_lens, so a captured call follows new lengths.
 //
-// Bound by memory.  Measured: one sequence of 1,000,001 tokens, 32 heads, bf16 188 us (6.1 TB/s); 64 of 1,024 to 16,384
-// tokens 129 us (5.4 TB/s; 5.9 while this kernel runs); 128 of 1 to 8,000 tokens, 2 x 16 rows, e4m3, pages of 16 82 us
-// (4.3 TB/s).  What is over the copy rate: 4 us until the first loads, 8,000 cycles where a CTA passes from one sequence to
+// Bound by memory.  Measured, calls in a row: one sequence of 1,000,001 tokens, 32 heads, bf16 184 us (6.3 TB/s); 64 of
+// 1,024 to 16,384 tokens 125 us (5.6 TB/s; 5.9 while this kernel runs); 128 of 1 to 8,000 tokens, 2 x 16 rows, e4m3, pages
+// of 16 80 us (4.4 TB/s).  A call alone on new inputs and a cold L2 takes 207, 133 and 95 us.  What is over the copy rate: 4 us until the first loads, 8,000 cycles where a CTA passes from one sequence to
 // the next and its rings stand full, 7 us from the first CTA's end to the joined result.
 //
 // Roles of a CTA's 11 warps: 0-3 and 4-7 softmax, rescaling and output, each group of four for half of the rows and

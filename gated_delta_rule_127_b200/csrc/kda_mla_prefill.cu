@@ -30,9 +30,10 @@
 // would stand alone).  The grid has a block for every item; a running CTA takes over blocks that have not begun yet
 // (cluster launch control), which balances them; the blocks' order puts the large items first.
 //
-// Bound by the tensor core and the power that it draws.  Measured, causal, 32 heads: 8,192 tokens 585 us (1,170 TFLOP/s,
-// 71% of what a library's matrix product reaches in a burst, 84% of what it sustains), eight prompts of 63 to 2,500
-// tokens 305 us, 2,048 queries over up to 32,048 keys 1,144 us (1,140 TFLOP/s); a box that throttles adds up to a tenth.
+// Bound by the tensor core and the power that it draws.  Measured, causal, 32 heads, calls in a row: 8,192 tokens 585 us
+// (1,170 TFLOP/s, 71% of what a library's matrix product reaches in a burst, 84% of what it sustains), eight prompts of 63
+// to 2,500 tokens 301 us, 2,048 queries over up to 32,048 keys 1,149 us (1,130 TFLOP/s).  A call alone on new inputs and a
+// cold L2 takes 642, 362 and 1,207 us.
 //
 // Roles of the 12 warps: 0-3 and 4-7 the sides' softmax and output, 8 finds the items and loads (TMA), 9 and 10 issue the
 // sides' products, 11 reports the loads' arrival.
@@ -49,8 +50,9 @@ using namespace sm100;
 
 constexpr int ROWS = 128;              // queries per side, keys per tile
 constexpr int THREADS = 384;
-// Steps in which the work is ordered by size.  1, one head after another: 672 us for 8,192 tokens, 308 for the eight
-// prompts, 1,104 for the long keys; 4: 585, 305, 1,144; 16: the eight prompts 340, as heads' keys and values are shared less.
+// Steps in which the work is ordered by size.  In turn on the same inputs after a flush of L2: 1, one head after another,
+// 629 us for 8,192 tokens, 337 for the eight prompts; 4: 563, 311; 16: 552, 337, as heads' keys and values are shared less.
+// The long keys are in one order whatever the steps, all pairs seeing about as many tiles (1,055, 1,055, 1,067 us).
 constexpr int LEVELS = 4;
 constexpr int PIECE = 16384, PIECES = 8, PER_TILE = 5;
 constexpr int OFF_RING = 2 * 3 * PIECE;                   // after both sides' queries (three blocks of 64 channels each)

@@ -108,8 +108,8 @@ def kda_version() -> int:
 
 
 def kda_testing_set_wait_limit(polls: int) -> None:
-    """Test hook (include/kda_testing.h): polls >= 0 bounds the prefill kernels' consumer-side waits at
-    that many polls (0: they give up at once); a negative value restores the default."""
+    """Test hook (include/kda_testing.h): polls >= 0 bounds the consumer-side waits of the prefill kernels
+    and of kda_mla_decode at that many polls (0: they give up at once); a negative value restores the default."""
     load_library().kda_testing_set_wait_limit(int(polls))
 
 

@@ -282,7 +282,7 @@ KDA_API kda_status kda_decode_step_ex(const void* q, const void* k, const void* 
  *   page_size a power of two from 16 to 1024; num_pages * page_size, max_pages * page_size and the packed rows T,
  *   Tq, Tk at most 2^31 - 256; d_latent = 512, d_pe = 64 (other sizes: KDA_ERR_UNSUPPORTED).
  * cu_seqlens of these entry points: [B + 1] int32 (device) or NULL (equal lengths, T a multiple of B), as in
- * kda_chunk_fwd, but cu_seqlens[B] may be less than T: the rows behind it are neither read nor written.
+ * kda_chunk_fwd, but cu_seqlens[B] may be less than T: the rows behind it are not written, and may hold anything.
  * Outputs, cache_* of a write and the workspace may overlap neither inputs nor one another (KDA_ERR_INVALID_ARG).
  * What only the device can see (cu_seqlens, lengths, page numbers) raises KDA_DEVFLAG_CU_SEQLENS,
  * KDA_DEVFLAG_SEQ_LENS or KDA_DEVFLAG_PAGE_TABLE; nothing outside the given arrays is touched.  The rows of
